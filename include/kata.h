@@ -444,6 +444,118 @@ kata_status_t kata_decode_step_sg(const void* q, const void* k, const void* v, v
                                   kata_dtype_t dtype, void* stream);
 
 /*
+ * Linear attention with a decay for each head.  For every sequence and head,
+ * with a = exp(log_decay[h]) (log_decay: [H] fp32 on the device, natural
+ * logarithm, <= 0; 0 keeps everything, -infinity keeps only the current token):
+ *   S_t = a S_{t-1} + k_t v_t^T,   o_t = scale * q_t^T S_t.
+ * No denominator: the state S [d, dv] is all a sequence carries.  A decay
+ * that is positive or NaN counts as 0 and records KATA_ERR_INVALID_ARG in
+ * the status word of kata_get_status().
+ *
+ * Packed sequences: q, k [T, H, d], v, o [T, H, dv], sequence n being the
+ * tokens cu_seqlens[n] .. cu_seqlens[n+1]-1 (cu_seqlens: N+1 int32 on the
+ * device, not decreasing, within 0..T; NULL with N = 1: all T tokens).
+ * Lengths of 0 are allowed.  Entries that decrease or leave 0..T are taken
+ * as their running maximum within those limits and record
+ * KATA_ERR_INVALID_ARG.  Rows outside every sequence are never read into a
+ * result (they may hold anything, NaN included); their rows of o are written
+ * as zeros when zero_outside != 0 and left as they were otherwise.
+ * q_stride, k_stride, v_stride, o_stride: elements from one token to the
+ * next (at least H*d or H*dv, a multiple of 8), so that the parts of a fused
+ * projection can be used in place.
+ *
+ * kata_fwd_linear_decay: prompts.  States: S0 (NULL: all start from zero) and
+ * S_out (NULL: not wanted) are pools [n_slots, H, d, dv] fp32; sequence n
+ * uses row slots[n] of both (slots: N int32 on the device; NULL: row n).  A
+ * negative slot starts from zero and leaves no state.  resume (NULL: all of
+ * them) holds N bytes on the device: a sequence with 0 starts from zero
+ * though S0 is given.  S0 and S_out may be the same pool, otherwise they must not
+ * overlap.  A slot of n_slots or more, and with S_out a slot that an earlier
+ * sequence of the call names too, records KATA_ERR_INVALID_ARG and counts
+ * as negative.  A sequence of length 0 leaves the state it starts from.
+ * bf16; d and dv in {64, 128}; others KATA_ERR_UNSUPPORTED.  Tensor-core
+ * arithmetic with fp32 accumulation; the state is carried in fp32, k scaled
+ * by its decay enters it as a sum of two bf16 values, and a bf16 copy of it
+ * is multiplied by q.
+ * workspace: kata_fwd_linear_decay_workspace_size() bytes (0 for short
+ * calls: NULL allowed), 256-byte aligned.  Repeated calls give bitwise the
+ * same result.
+ */
+size_t kata_fwd_linear_decay_workspace_size(int T, int H, int d, int dv, int N);
+kata_status_t kata_fwd_linear_decay(const void* q, const void* k, const void* v, void* o,
+                                    int T, int H, int d, int dv,
+                                    long long q_stride, long long k_stride, long long v_stride, long long o_stride,
+                                    const float* log_decay, float scale, const int* cu_seqlens, int N,
+                                    const float* S0, float* S_out, const int* slots, int n_slots,
+                                    const unsigned char* resume, int zero_outside, kata_dtype_t dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of kata_fwd_linear_decay for dO [T, H, dv] (and dS_out, the
+ * gradient of the final states, NULL: zero):
+ *   R_t = a R_{t+1} + scale q_t dO_t^T   (backwards, entered by dS_out)
+ *   dq_t = scale S_t dO_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dS0 = a R_1.
+ * S0, dS_out, dS0 (NULL: not wanted): [N, H, d, dv] fp32, one row per
+ * sequence.  dO, dq, dk [T, H, d] and dv are contiguous; q, k, v as in the
+ * forward.  Rows outside every sequence get zero gradients.  The decays are
+ * constants: they get no gradient.  Types, sizes, workspace
+ * (kata_bwd_linear_decay_workspace_size()) and errors as in the forward.
+ */
+size_t kata_bwd_linear_decay_workspace_size(int T, int H, int d, int dv, int N);
+kata_status_t kata_bwd_linear_decay(const void* q, const void* k, const void* v, const void* dO,
+                                    void* dq, void* dk, void* dv, int T, int H, int d, int dv_width,
+                                    long long q_stride, long long k_stride, long long v_stride,
+                                    const float* log_decay, float scale, const int* cu_seqlens, int N,
+                                    const float* S0, const float* dS_out, float* dS0, kata_dtype_t dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of n streams, in place on the pool of states:
+ *   S <- a S + k v^T,  o = scale * q^T S     (S = S[slots[i]], [H, d, dv]).
+ * q, k [n, H, d]; v, o [n, H, dv] (bf16 or fp32; strides between streams as
+ * above, a multiple of 16 bytes); S [n_slots, H, d, dv] fp32; slots: n int32
+ * on the device (NULL: row i).  A stream with a negative slot is padding:
+ * its row of o is written as zeros and no state is touched.  A slot of
+ * n_slots or more, or one that an earlier stream of the call names too,
+ * counts as negative and records KATA_ERR_INVALID_ARG in the status word.
+ * d and dv in {64, 128}; fp32 arithmetic throughout.
+ */
+kata_status_t kata_decode_step_linear_decay(const void* q, const void* k, const void* v, void* o, float* S,
+                                            int n, int H, int d, int dv,
+                                            long long q_stride, long long k_stride, long long v_stride,
+                                            long long o_stride, const float* log_decay, float scale,
+                                            const int* slots, int n_slots, kata_dtype_t dtype, void* stream);
+
+/*
+ * An 8-bit cache of states, for prefixes that are used again and streams that
+ * wait: a quarter of the memory of the fp32 pool.  For any pool of this
+ * library, S [n_slots, H, rows, dv] fp32 (rows = d of the linear states, p*p
+ * or groups*p*p of the KATA states), and, when there is one, its z
+ * [n_slots, H, rows]; the cache holds cache [n_entries, H, rows, dv] int8,
+ * scale [n_entries, H, rows] fp32 and z_cache [n_entries, H, rows] fp32.
+ *
+ * kata_state_store_q8 writes slot slots[i] to entry entries[i], i < n:
+ *   scale = max_j |x_j| / 127, rounded to fp32;  c_j = x_j / scale rounded
+ * to the nearest integer, ties to even, exactly (the quotient is not rounded
+ * first).  A row with scale < 2^-126 is held as scale 0 and zeros; a row
+ * holding an infinity or a NaN is held as scale NaN and zeros, and reads back
+ * as NaN.  z is copied.  kata_state_load_q8 writes c_j * scale, rounded to
+ * fp32, to slot slots[i] from entry entries[i]; several slots may be loaded
+ * from one entry.
+ * slots, entries: n int32 on the device, NULL = i (bounded by the pool's
+ * size).  A pair with a negative index is skipped; a pair with an index out
+ * of range, or with a destination that an earlier pair names too, is skipped
+ * and records KATA_ERR_INVALID_ARG in the status word.  z and z_cache: both
+ * or neither.  dv in {16, 64, 128}, rows >= 1.
+ */
+kata_status_t kata_state_store_q8(const float* S, const float* z, int n_slots, signed char* cache, float* scale,
+                                  float* z_cache, int n_entries, const int* slots, const int* entries, int n,
+                                  int H, int rows, int dv, void* stream);
+kata_status_t kata_state_load_q8(const signed char* cache, const float* scale, const float* z_cache, int n_entries,
+                                 float* S, float* z, int n_slots, const int* entries, const int* slots, int n,
+                                 int H, int rows, int dv, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device-side status word
  * of the current device (KATA_ERR_TIMEOUT if a bounded wait in a kernel ran
  * out since the last call), or KATA_ERR_CUDA if the stream reports an error.

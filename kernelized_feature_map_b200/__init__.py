@@ -33,7 +33,14 @@ The computation lives in ``libkata.so`` (hand-written CUDA behind the C ABI of
   :func:`kata_attention_mg` -- the same for KATA-Mg ([B,H,T,d]);
 * :func:`kata_fwd_linear_chunked`, :func:`kata_fwd_linear_chunked_sequential`
   -- first-order (psi(u) = u) attention, chunked with the associative scan
-  and its matched sequential baseline.
+  and its matched sequential baseline;
+* :func:`kata_fwd_linear_decay`, :func:`kata_bwd_linear_decay`,
+  :func:`kata_attention_linear_decay`, :func:`kata_decode_step_linear_decay`
+  -- linear attention with a decay for each head: packed prompts, their
+  gradients (and the autograd wrapper) and the single-token step on a pool of
+  states;
+* :func:`kata_state_store_q8`, :func:`kata_state_load_q8` -- an 8-bit cache
+  for the states of any of these paths.
 """
 from ._abi import (KataError, kata_abi_version, kata_decode_step, kata_fwd_chunked,  # noqa: F401
                    kata_fwd_chunked_noalloc, kata_fwd_chunked_sequential, kata_fwd_chunked_workspace_size,
@@ -47,3 +54,6 @@ from ._abi import (KataError, kata_abi_version, kata_decode_step, kata_fwd_chunk
                    kata_fwd_linear_chunked, kata_fwd_linear_chunked_sequential,
                    kata_fwd_linear_chunked_workspace_size,
                    kata_get_status, kata_set_wait_limit, lib, status_string)
+from ._decay import (KataAttentionLinearDecay, kata_attention_linear_decay, kata_bwd_linear_decay,  # noqa: F401
+                     kata_bwd_linear_decay_workspace_size, kata_decode_step_linear_decay, kata_fwd_linear_decay,
+                     kata_fwd_linear_decay_workspace_size, kata_state_load_q8, kata_state_store_q8)

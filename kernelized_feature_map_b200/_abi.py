@@ -22,6 +22,7 @@ KATA_LAYOUT_BHTD, KATA_LAYOUT_BTHD = 0, 1
 
 # name -> (restype, argtypes), mirroring include/kata.h
 _c_int, _c_size, _vp, _fp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p
+_c_ll, _c_float = ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "kata_fwd_quadratic": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
     "kata_fwd_chunked_workspace_size": (_c_size, [_c_int] * 7),
@@ -53,6 +54,17 @@ SIGNATURES = {
     "kata_fwd_sg_quadratic_train": (_c_int, [_vp, _vp, _vp, _vp, _fp] + [_c_int] * 7 + [_vp]),
     "kata_bwd_sg_quadratic": (_c_int, [_vp] * 9 + [_c_int] * 7 + [_vp, _c_size, _vp]),
     "kata_fwd_sg_chunked": (_c_int, [_vp, _vp, _vp, _vp] + [_c_int] * 8 + [_fp, _fp, _fp, _fp, _vp, _c_size, _vp]),
+    "kata_fwd_linear_decay_workspace_size": (_c_size, [_c_int] * 5),
+    "kata_fwd_linear_decay": (_c_int, [_vp] * 4 + [_c_int] * 4 + [_c_ll] * 4 + [_fp, _c_float, _vp, _c_int, _fp, _fp,
+                                                                               _vp, _c_int, _vp, _c_int, _c_int, _vp,
+                                                                               _c_size, _vp]),
+    "kata_bwd_linear_decay_workspace_size": (_c_size, [_c_int] * 5),
+    "kata_bwd_linear_decay": (_c_int, [_vp] * 7 + [_c_int] * 4 + [_c_ll] * 3 + [_fp, _c_float, _vp, _c_int, _fp, _fp,
+                                                                               _fp, _c_int, _vp, _c_size, _vp]),
+    "kata_decode_step_linear_decay": (_c_int, [_vp] * 4 + [_fp] + [_c_int] * 4 + [_c_ll] * 4
+                                      + [_fp, _c_float, _vp, _c_int, _c_int, _vp]),
+    "kata_state_store_q8": (_c_int, [_fp, _fp, _c_int, _vp, _fp, _fp, _c_int, _vp, _vp] + [_c_int] * 4 + [_vp]),
+    "kata_state_load_q8": (_c_int, [_vp, _fp, _fp, _c_int, _fp, _fp, _c_int, _vp, _vp] + [_c_int] * 4 + [_vp]),
     "kata_get_status": (_c_int, [_vp]),
     "kata_status_string": (ctypes.c_char_p, [_c_int]),
     "kata_set_wait_limit": (None, [ctypes.c_longlong]),

@@ -177,6 +177,55 @@ cudaError_t launch_chunk_readout_cluster(const void* q, const void* k, const voi
                                          const ChunkPlan& pl, int H, int groups, bool bthd, const WaitCtl& wc,
                                          cudaStream_t st);
 
+// state_q8.cu -- pools of states to and from the 8-bit cache; rows = H * rows of a head.
+cudaError_t launch_state_store_q8(const float* S, const float* z, int n_slots, signed char* cache, float* scale,
+                                  float* z_cache, int n_entries, const int* slots, const int* entries, int n,
+                                  long long rows, int dv, const WaitCtl& wc, cudaStream_t st);
+cudaError_t launch_state_load_q8(const signed char* cache, const float* scale, const float* z_cache, int n_entries,
+                                 float* S, float* z, int n_slots, const int* entries, const int* slots, int n,
+                                 long long rows, int dv, const WaitCtl& wc, cudaStream_t st);
+
+// decay_step.cu -- one token of linear attention with a per-head decay.
+cudaError_t launch_decay_step(const void* q, const void* k, const void* v, void* o, float* S, int n, int H, int d,
+                              int dv, long long q_stride, long long k_stride, long long v_stride, long long o_stride,
+                              const float* log_decay, float scale, const int* slots, int n_slots, kata_dtype_t dt,
+                              const WaitCtl& wc, cudaStream_t st);
+
+// Linear attention with a per-head decay over packed sequences: one walk is
+//   out_t = scale * sum_{s <= t} a^(t-s) (A_t . B_s) C_s  +  (entering state)
+// or, reversed, the same over s >= t.  The forward is the walk (q, k, v); the
+// gradients are the walks dq: (dO, v, k), dk: reversed (v, dO, q) and dv:
+// reversed (k, q, dO), since each of the three factors of a pair's term
+// a^(t-s) (q_t . k_s) (v_s . dO_t) enters linearly.
+struct DecayWalk {
+  const void *a, *b, *c;  // bf16 [T, H, d1], [T, H, d1], [T, H, d2]
+  void* out;              // bf16 [T, H, d2]
+  long long a_stride, b_stride, c_stride, out_stride;  // elements per token
+  int d1, d2;
+  bool reverse;
+  // The state entering a sequence, [rows, H, d1, d2] fp32 ([.., d2, d1] when
+  // init_transposed), null: zero.  Forward it is S before the first token;
+  // reversed it is the gradient of the state after the last token.
+  const float* init;
+  bool init_transposed;
+  float* fin;  // the state leaving it (reversed: the gradient of the state before the first token), or null
+};
+struct DecayShape {
+  int T, H, N;
+  const int* cu;             // [N + 1] or null
+  const float* log_decay;    // [H]
+  float scale;
+  const int* slots;          // pool row of each sequence or null
+  int n_slots;
+  const unsigned char* resume;
+  bool zero_outside;
+};
+size_t decay_workspace_bytes(int T, int H, int d1, int d2, int N, int walks);
+cudaError_t launch_decay_walks(const DecayWalk* walks, int n, const DecayShape& sh, void* ws, const WaitCtl& wc,
+                               cudaStream_t st);
+// Sequences of no tokens at all (T = 0): fin = init or zero.
+cudaError_t launch_decay_empty(const DecayWalk& w, const DecayShape& sh, const WaitCtl& wc, cudaStream_t st);
+
 // Current bound on in-kernel waits and the status word (kata_api.cu).
 WaitCtl wait_ctl();
 
