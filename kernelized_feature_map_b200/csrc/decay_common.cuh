@@ -47,47 +47,51 @@ __device__ __forceinline__ bool seq_range(const int* __restrict__ cu, int n0, in
   return n >= N || (c0 >= 0 && c1 <= T && c0 <= c1);
 }
 
-// The target-th segment when every sequence is cut into segments of L tokens
-// (an empty sequence is one empty segment).  Called by a whole warp; the
-// result is the same in all lanes.  first/last receive the first token of the
-// first sequence and the end of the last one seen (the last sequence's end
-// when it holds the target).
-__device__ __forceinline__ Segment find_segment(const int* __restrict__ cu, int N, int T, int L, int target, int lane,
-                                                bool& valid) {
+// What find_segment counts: segments (an empty sequence is one empty segment)
+// or only the sequences that are cut into more than one.
+enum FindWhat { kSegments, kSplitSequences };
+
+// The target-th segment, or the first segment of the target-th split
+// sequence, when every sequence is cut into segments of L tokens.  Called by
+// a whole warp; the result is the same in all lanes.  `valid` is false where
+// cu's entries up to the target had to be mended.
+__device__ __forceinline__ Segment find_segment(const int* __restrict__ cu, int N, int T, int L, FindWhat what,
+                                                int target, int lane, bool& valid) {
   Segment r{-1, 0, 0, 0, 0, 0, 0, 0};
-  int carry = 0, segs = 0, recs = 0;
+  int carry = 0, counted = 0, recs = 0;
   valid = true;
   for (int n0 = 0; n0 < N; n0 += 32) {
     int s0, s1;
     const bool ok = seq_range(cu, n0, N, T, carry, lane, s0, s1);
     valid = valid && __all_sync(0xffffffffu, ok);
     const int n = n0 + lane;
-    const int mine = n < N ? max(1, (s1 - s0 + L - 1) / L) : 0;
-    const int rec = mine > 1 ? mine : 0;
-    int ps = mine, pr = rec;  // inclusive prefix sums
+    const int segs = n < N ? max(1, (s1 - s0 + L - 1) / L) : 0;
+    const int rec = segs > 1 ? segs : 0;
+    const int mine = what == kSegments ? segs : segs > 1 ? 1 : 0;
+    int pc = mine, pr = rec;  // inclusive prefix sums
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, ps, o), y = __shfl_up_sync(0xffffffffu, pr, o);
+      const int x = __shfl_up_sync(0xffffffffu, pc, o), y = __shfl_up_sync(0xffffffffu, pr, o);
       if (lane >= o) {
-        ps += x;
+        pc += x;
         pr += y;
       }
     }
-    const bool here = n < N && target >= segs + ps - mine && target < segs + ps;
+    const bool here = target >= counted + pc - mine && target < counted + pc;
     const unsigned who = __ballot_sync(0xffffffffu, here);
     if (who) {
       const int src = __ffs(who) - 1;
       r.seq = n0 + src;
       r.s0 = __shfl_sync(0xffffffffu, s0, src);
       r.s1 = __shfl_sync(0xffffffffu, s1, src);
-      r.n_seg = __shfl_sync(0xffffffffu, mine, src);
-      r.seg = target - (segs + __shfl_sync(0xffffffffu, ps - mine, src));
+      r.n_seg = __shfl_sync(0xffffffffu, segs, src);
+      r.seg = what == kSegments ? target - (counted + __shfl_sync(0xffffffffu, pc - mine, src)) : 0;
       r.rec = recs + __shfl_sync(0xffffffffu, pr - rec, src);
       r.t0 = r.s0 + r.seg * L;
       r.t1 = min(r.s1, r.t0 + L);
       return r;
     }
-    segs += __shfl_sync(0xffffffffu, ps, 31);
+    counted += __shfl_sync(0xffffffffu, pc, 31);
     recs += __shfl_sync(0xffffffffu, pr, 31);
     carry = __shfl_sync(0xffffffffu, s1, 31);
   }

@@ -1,0 +1,761 @@
+// decay_walk_sm100.cu -- linear attention with a per-head decay over packed
+// sequences, chunk by chunk on tcgen05 / TMEM.
+//
+// One walk (kata_internal.h) computes out_t = scale * sum_{s<=t} a^(t-s)
+// (A_t . B_s) C_s plus the reach of the entering state, or the same over
+// s >= t, backwards.  A sequence is walked in chunks of 128 tokens with the
+// state S [d1, d2] in between.  For a chunk of r tokens (rows i, j; forward):
+//   P     = A B^T                              [128 x 128]
+//   W_ij  = a^(i-j) P_ij for j <= i, else 0    rounded to bf16
+//   out_i = scale (sum_j W_ij C_j + a^(i+1) A_i S)
+//   S     = a^r S + sum_j (a^(r-1-j) B_j) C_j^T
+// and backwards, where the entering state already belongs to the chunk's last
+// token: W_ij = a^(j-i) P_ij for j >= i, the reach of S is a^(r-1-i) and B_j
+// enters with a^(j+1), times the scale (S is then the gradient itself, which
+// the entering gradient joins unscaled).
+//
+// Roundings.  S is fp32, in TMEM for the whole walk: the tensor cores
+// accumulate onto it.  The scaled B_j would lose 2^-9 of the state if it went
+// in as one bf16; it goes in as two, hi + lo (error 2^-17, the state agrees
+// with fp32 arithmetic), at the price of a second pass of that product.  W
+// and the copy of S that A is multiplied with are rounded to bf16 once: they
+// reach only out, which is rounded as far itself.
+//
+// One CTA per segment of a sequence, head and walk (1 CTA per SM: 512 TMEM
+// columns).  Warps (576 threads):
+//   0       TMA: A, B, C tiles of the chunks into a ring of kStages
+//   1       TMEM allocator; MMA issue (whole warp, one elected lane)
+//   2-9     W from P (two warps per TMEM lane quarter, half of the columns
+//           each), and out from the two accumulators
+//   10-13   S: the bf16 copy for the next chunk, and its scaling in TMEM
+//   14-17   B: hi in place over the tile once P is done, lo over the A tile once
+//           A has met S; rows past the sequence's end cleared in B and C,
+//           so that nothing of the next sequence (NaN included) gets in
+// MMA order per chunk: P; A S; hi; W C; lo.  The state of the next chunk
+// waits only for lo, and while it is copied and scaled P and W of the next
+// chunk proceed.
+//
+// TMEM columns: P (W over it) 128 | W C d2 | A S d2 | S d2.  With d1 = 64 the
+// state product still has 128 rows: its A operand reads the 64 columns twice
+// (leading offset 0), so lanes 64-127 hold a second copy of S, and the two
+// halves of the warps write one half of the bf16 copy each.
+//
+// Long sequences with few heads do not fill the SMs: they are cut into
+// segments of L tokens.  decay_walk_kernel<.., true> first sums each segment
+// from a zero state, decay_scan_kernel turns the sums into the states entering
+// the segments, and the walks start from those (kata_internal.h, plan below).
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "decay_common.cuh"
+#include "kata_internal.h"
+#include "sm100.cuh"
+
+namespace kata {
+namespace {
+
+using namespace sm100;
+
+constexpr int kChunk = 128;
+constexpr int kThreads = 576;
+constexpr int kMaxWalks = 3;
+constexpr uint32_t kTmemCols = 512;
+
+struct WalkParams {
+  CUtensorMap a, b, c;
+  __nv_bfloat16* out;
+  long long out_stride;
+  const float* init;
+  float* fin;
+  float* rec;            // records of this walk's split sequences, [segment][H][d1][d2]
+  int swapped;           // this walk has (d1, d2) of the kernel exchanged
+  int reverse, init_transposed;
+  float s_intra, s_inter, s_key;
+};
+
+struct Params {
+  WalkParams w[kMaxWalks];
+  const int* cu;
+  const float* log_decay;
+  const int* slots;
+  const unsigned char* resume;
+  int n_walks, T, H, N, L, n_slots, zero_outside;
+  WaitCtl wc;
+};
+
+template <int D1, int D2>
+struct Cfg {
+  static constexpr int kA = kChunk * D1 * 2, kC = kChunk * D2 * 2;  // tile bytes
+  static constexpr int kStage = 2 * kA + kC;                         // [A | B | C]
+  static constexpr int kCopy = D1 * D2 * 2;
+  static constexpr int kFit = (226 * 1024 - kCopy) / kStage;
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;                // 2 (128, 128) .. 4 (64, 64)
+  static constexpr int offStage = 0;
+  static constexpr int offCopy = kStages * kStage;
+  static constexpr int offPow = offCopy + kCopy;        // a^0 .. a^128
+  static constexpr int offCol = offPow + 132 * 4;       // column factors of a full 32-column block
+  static constexpr int offBar = offCol + 32 * 4;
+  static constexpr int kBars = 2 * kStages + 10;
+  static constexpr int offMisc = offBar + kBars * 8;
+  static constexpr int kBytes = offMisc + 64 + 1024;    // + alignment slack
+  static constexpr uint32_t colP = 0, colI = 128, colE = 128 + D2, colS = 128 + 2 * D2;
+};
+static_assert(Cfg<128, 128>::kStages >= 2 && Cfg<128, 128>::kBytes <= 227 * 1024, "shared memory");
+static_assert(Cfg<128, 64>::kBytes <= 227 * 1024 && Cfg<64, 128>::kBytes <= 227 * 1024, "shared memory");
+static_assert(Cfg<64, 64>::kBytes <= 227 * 1024, "shared memory");
+
+struct Found {
+  int seq, s0, s1, seg, n_seg, t0, t1, rec, row, resumed;
+};
+
+// 16-byte unit u (8 values) of row r in a tile of 128-byte swizzled rows, `rows` to a 64-column atom
+__device__ __forceinline__ uint32_t unit_offset(int rows, int r, int u) {
+  return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+}
+
+template <int D1, int D2, bool kSum>
+__device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem, const Found& f) {
+  using C = Cfg<D1, D2>;
+  constexpr int kStages = C::kStages;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::offBar);
+  uint64_t* full = bars;               // [kStages] tiles landed
+  uint64_t* empty = full + kStages;    // [kStages] tiles read
+  uint64_t* p_full = empty + kStages;  // P in TMEM
+  uint64_t* w_full = p_full + 1;       // W written (256)
+  uint64_t* s_ready = w_full + 1;      // S scaled and copied (128)
+  uint64_t* a_done = s_ready + 1;      // A has met B and S: its tile takes lo
+  uint64_t* hi_full = a_done + 1;      // hi written, rows past the end cleared (128)
+  uint64_t* lo_full = hi_full + 1;     // lo written (128)
+  uint64_t* o_full = lo_full + 1;      // both accumulators of out complete
+  uint64_t* o_free = o_full + 1;       // and read (256)
+  uint64_t* s_done = o_free + 1;       // S advanced
+  uint64_t* mma_done = s_done + 1;     // every MMA issued has completed
+  float* pw = reinterpret_cast<float*>(smem + C::offPow);
+  float* col = reinterpret_cast<float*>(smem + C::offCol);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::offMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offMisc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool rev = w.reverse != 0;
+  const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
+  // c-th chunk walked: its first token and its tokens
+  auto chunk_t = [&](int c) { return f.t0 + (rev ? n_chunks - 1 - c : c) * kChunk; };
+  auto chunk_n = [&](int c) { return min(kChunk, f.t1 - chunk_t(c)); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(p_full, 1);
+    mbar_init(w_full, 256);
+    mbar_init(s_ready, 128);
+    mbar_init(a_done, 1);
+    mbar_init(hi_full, 128);
+    mbar_init(lo_full, 128);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, 256);
+    mbar_init(s_done, 1);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  const float g = used_log_decay(p.log_decay[h], p.wc.status);
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + 129) pw[threadIdx.x - 64] = expf(g * (float)(threadIdx.x - 64));
+  if (threadIdx.x >= 224 && threadIdx.x < 256) {
+    const int j = threadIdx.x - 224;
+    col[j] = expf(g * (float)(rev ? j : 31 - j));
+  }
+  if (warp == 1) tmem_alloc(tmem_holder, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const WaitEnv env{p.wc.status, abort_flag, p.wc.limit};
+
+  if (warp == 0) {
+    // --------------------------------------------------------------- TMA
+    if (lane == 0) {
+      int issued = 0;
+      for (int c = 0; c < n_chunks; ++c) {
+        const int st = c % kStages;
+        if (!mbar_wait(empty + st, ((c / kStages) & 1) ^ 1, env)) break;
+        uint8_t* base = smem + C::offStage + st * C::kStage;
+        const int t = chunk_t(c);
+        mbar_arrive_expect_tx(full + st, kSum ? C::kA + C::kC : C::kStage);
+#pragma unroll
+        for (int x = 0; x < D1 / 64; ++x) {
+          if (!kSum) tma_load_3d(base + x * 16384, &w.a, full + st, 64 * x, h, t);
+          tma_load_3d(base + C::kA + x * 16384, &w.b, full + st, 64 * x, h, t);
+        }
+#pragma unroll
+        for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + 2 * C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
+        ++issued;
+      }
+      // every copy this CTA started must land before it exits
+      for (int c = issued - kStages < 0 ? 0 : issued - kStages; c < issued; ++c)
+        mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA
+    constexpr uint32_t id_p = idesc_bf16(128, 128, false, false);  // A, B both K-major
+    constexpr uint32_t id_o = idesc_bf16(128, D2, false, true);    // A or W, and C or the copy of S (N-major)
+    constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);     // B^T (M-major), C (N-major)
+    constexpr uint32_t kAtom = D1 == 128 ? 16384u : 0u;            // second 64 rows of the state: see above
+    const uint32_t sStage = smem_u32(smem + C::offStage), sCopy = smem_u32(smem + C::offCopy);
+    const uint64_t dcopy = smem_desc(sCopy, D1 * 128, 1024, kSw128);
+    for (int c = 0; c < n_chunks; ++c) {
+      const int st = c % kStages;
+      const uint32_t sA = sStage + st * C::kStage, sB = sA + C::kA, sC = sB + C::kA;
+      const uint64_t dA = smem_desc(sA, 16, 1024, kSw128), dB = smem_desc(sB, 16, 1024, kSw128);
+      const uint64_t dC = smem_desc(sC, 16384, 1024, kSw128);
+      const uint64_t dHi = smem_desc(sB, kAtom, 1024, kSw128), dLo = smem_desc(sA, kAtom, 1024, kSw128);
+      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
+      tc_fence_after();
+      if (!kSum) {
+        // over W of the chunk before only after its products, issued before
+#pragma unroll
+        for (int ks = 0; ks < D1 / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+          mma_ss_w(tmem + C::colP, desc_add(dA, off), desc_add(dB, off), id_p, ks > 0);
+        }
+        mma_commit_w(p_full);
+      }
+      if (!mbar_wait_w(s_ready, c & 1, env)) break;
+      if (!kSum) {
+        if (c > 0 && !mbar_wait_w(o_free, (c - 1) & 1, env)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < D1 / 16; ++ks)
+          mma_ss_w(tmem + C::colE, desc_add(dA, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dcopy, ks * 2048), id_o,
+                   ks > 0);
+        mma_commit_w(a_done);
+      }
+      if (!mbar_wait_w(hi_full, c & 1, env)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < kChunk / 16; ++ks)
+        mma_ss_w(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+      if (!kSum) {
+        if (!mbar_wait_w(w_full, c & 1, env)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < kChunk / 16; ++ks)  // keys 16 ks ..: W columns 64 (ks / 4) + 8 (ks % 4)
+          mma_ts_w(tmem + C::colI, tmem + C::colP + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(dC, ks * 2048), id_o,
+                   ks > 0);
+        mma_commit_w(o_full);
+      }
+      if (!mbar_wait_w(lo_full, c & 1, env)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < kChunk / 16; ++ks)
+        mma_ss_w(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+      mma_commit_w(s_done);
+      mma_commit_w(empty + st);
+    }
+    mma_commit_w(mma_done);
+    mbar_wait_drain(mma_done, 0);
+  } else if (warp < 10) {
+    // --------------------------------------------------------------- W and out
+    const int quarter = warp % 4, half = warp >= 6 ? 1 : 0;
+    const int i = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    // a^(i-j) = a^(i-j1) a^(j1-j) for the columns j0 .. j1 = j0 + 31 of a block
+    // left of the diagonal, both exponents >= 0; backwards a^(j-i) =
+    // a^(j0-i) a^(j-j0) right of it: a factor of the row, constant over the
+    // chunks, and one of the column, the same for all blocks
+    float row_f[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int j0 = 32 * (2 * half + b), e = rev ? j0 - i : i - j0 - 31;
+      row_f[b] = e >= 0 ? pw[e] : 0.f;
+    }
+    const float reach_f = pw[i + 1];
+    for (int c = 0; !kSum && c < n_chunks; ++c) {
+      const int n = chunk_n(c);
+      if (!mbar_wait_w(p_full, c & 1, env)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int bb = 2 * half + b;
+        uint32_t x[16];
+        if (rev ? bb < quarter : bb > quarter) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = 0u;
+        } else {
+          uint32_t r[32];
+          tmem_ld32(lane_base + C::colP + 32 * bb, r);
+          tmem_wait_ld();
+          if (bb != quarter) {
+            const uint64_t rf = f32x2(__float_as_uint(row_f[b]), __float_as_uint(row_f[b]));
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float4 cf = reinterpret_cast<const float4*>(col)[e / 2];
+              const uint64_t lo = f32x2_mul(f32x2_mul(f32x2(r[2 * e], r[2 * e + 1]), rf),
+                                            f32x2(__float_as_uint(cf.x), __float_as_uint(cf.y)));
+              const uint64_t hi = f32x2_mul(f32x2_mul(f32x2(r[2 * e + 2], r[2 * e + 3]), rf),
+                                            f32x2(__float_as_uint(cf.z), __float_as_uint(cf.w)));
+              x[e] = pack_bf16x2(f32x2_lo(lo), f32x2_hi(lo));
+              x[e + 1] = pack_bf16x2(f32x2_lo(hi), f32x2_hi(hi));
+            }
+            if (rev && 32 * bb + 32 > n) {  // columns past the end hold another sequence's rows
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int j = 32 * bb + 2 * e;
+                x[e] = j >= n ? 0u : j + 1 >= n ? x[e] & 0xffffu : x[e];
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float v[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int jj = 2 * e + y, away = rev ? jj - lane : lane - jj;
+                const bool keep = away >= 0 && (!rev || 32 * bb + jj < n);
+                v[y] = keep ? __uint_as_float(r[jj]) * pw[keep ? away : 0] : 0.f;
+              }
+              x[e] = pack_bf16x2(v[0], v[1]);
+            }
+          }
+        }
+        tmem_st16(lane_base + C::colP + 64 * half + 16 * b, x);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(w_full);
+      // out = s_intra W C + s_inter a^reach A S
+      if (!mbar_wait_w(o_full, c & 1, env)) break;
+      tc_fence_after();
+      const float reach = w.s_inter * (rev ? pw[max(n - 1 - i, 0)] : reach_f);
+      __nv_bfloat16* orow = w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + half * (D2 / 2);
+#pragma unroll
+      for (int b = 0; b < D2 / 64; ++b) {
+        uint32_t x[32], y[32];
+        tmem_ld32(lane_base + C::colI + half * (D2 / 2) + 32 * b, x);
+        tmem_ld32(lane_base + C::colE + half * (D2 / 2) + 32 * b, y);
+        tmem_wait_ld();
+        if (b == D2 / 64 - 1) {
+          tc_fence_before();
+          mbar_arrive(o_free);
+        }
+        if (i < n) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              z[k] = pack_bf16x2(
+                  fmaf(reach, __uint_as_float(y[e + 2 * k]), w.s_intra * __uint_as_float(x[e + 2 * k])),
+                  fmaf(reach, __uint_as_float(y[e + 2 * k + 1]), w.s_intra * __uint_as_float(x[e + 2 * k + 1])));
+            *reinterpret_cast<uint4*>(orow + 32 * b + e) = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+        }
+      }
+    }
+  } else if (warp < 14) {
+    // --------------------------------------------------------------- S
+    const int quarter = warp % 4;
+    const int m = quarter * 32 + lane, row = m % D1;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colS;
+    uint8_t* copy = smem + C::offCopy;
+    // columns of the row that this warp writes out (d1 = 64: each half of the lanes one half)
+    const int own0 = D1 == 64 && quarter >= 2 ? D2 / 2 : 0, own1 = D1 == 64 && quarter < 2 ? D2 / 2 : D2;
+    const long long size = (long long)D1 * D2;
+    const bool split = f.n_seg > 1;
+    const float* src = nullptr;
+    bool transposed = false;
+    if (!kSum) {
+      griddep_wait();  // the segments' entering states (launched behind the scan, or behind nothing of this call)
+      if (split) {
+        src = w.rec + ((long long)(f.rec + f.seg) * p.H + h) * size;
+      } else if (w.init && f.row >= 0 && f.resumed) {
+        src = w.init + ((long long)f.row * p.H + h) * size;
+        transposed = w.init_transposed != 0;
+      }
+    }
+    float* dst = nullptr;
+    if (kSum)
+      dst = w.rec + ((long long)(f.rec + f.seg) * p.H + h) * size;
+    else if (w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1))
+      dst = w.fin + ((long long)f.row * p.H + h) * size;
+    if (n_chunks == 0 && dst) {  // an empty sequence leaves what it starts from
+      for (int j = own0; j < own1; ++j)
+        dst[(long long)row * D2 + j] = src ? src[transposed ? (long long)j * D1 + row : (long long)row * D2 + j] : 0.f;
+    }
+    for (int c = 0; c <= n_chunks && n_chunks > 0; ++c) {
+      // c = 0: the entering state; then the state after chunk c - 1
+      if (c > 0) {
+        if (!mbar_wait_w(s_done, (c - 1) & 1, env)) break;
+        tc_fence_after();
+      }
+      const float keep = c < n_chunks ? pw[chunk_n(c)] : 0.f;
+#pragma unroll 1
+      for (int b = 0; b < D2 / 32; ++b) {
+        uint32_t r[32];
+        if (c > 0) {
+          tmem_ld32(lane_base + 32 * b, r);
+          tmem_wait_ld();
+        } else if (src && !transposed) {
+          const float4* s4 = reinterpret_cast<const float4*>(src + (long long)row * D2 + 32 * b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 x = s4[e];
+            r[4 * e] = __float_as_uint(x.x);
+            r[4 * e + 1] = __float_as_uint(x.y);
+            r[4 * e + 2] = __float_as_uint(x.z);
+            r[4 * e + 3] = __float_as_uint(x.w);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            r[e] = src ? __float_as_uint(src[(long long)(32 * b + e) * D1 + row]) : 0u;
+        }
+        const bool own = 32 * b >= own0 && 32 * b < own1;
+        if (c == n_chunks) {
+          if (dst && own) {
+            float4* d4 = reinterpret_cast<float4*>(dst + (long long)row * D2 + 32 * b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              d4[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                  __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
+          }
+          continue;
+        }
+        if (!kSum && own) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
+            *reinterpret_cast<uint4*>(copy + unit_offset(D1, row, 4 * b + e)) = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t z[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(keep * __uint_as_float(r[16 * s + e]));
+          tmem_st16(lane_base + 32 * b + 16 * s, z);
+        }
+      }
+      if (c == n_chunks) break;
+      tmem_wait_st();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(s_ready);
+    }
+  } else {
+    // --------------------------------------------------------------- B
+    const int j = (warp - 14) * 32 + lane;  // token of the chunk
+    for (int c = 0; c < n_chunks; ++c) {
+      const int st = c % kStages, n = chunk_n(c);
+      uint8_t* tA = smem + C::offStage + st * C::kStage;
+      uint8_t *tB = tA + C::kA, *tC = tB + C::kA;
+      const float fac = j < n ? w.s_key * (rev ? pw[j + 1] : pw[n - 1 - j]) : 0.f;
+      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
+      if (!kSum && !mbar_wait_w(p_full, c & 1, env)) break;
+      if (j >= n) {
+#pragma unroll
+        for (int u = 0; u < D2 / 8; ++u)
+          *reinterpret_cast<uint4*>(tC + unit_offset(kChunk, j, u)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      uint4 lo[D1 / 8];
+#pragma unroll
+      for (int u = 0; u < D1 / 8; ++u) {
+        uint4* at = reinterpret_cast<uint4*>(tB + unit_offset(kChunk, j, u));
+        const uint4 x = *at;
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h4[4], l4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a0 = fac * __uint_as_float(in[k] << 16), a1 = fac * __uint_as_float(in[k] & 0xffff0000u);
+          if (j >= n) a0 = a1 = 0.f;
+          h4[k] = pack_bf16x2(a0, a1);
+          l4[k] = pack_bf16x2(a0 - __uint_as_float(h4[k] << 16), a1 - __uint_as_float(h4[k] & 0xffff0000u));
+        }
+        *at = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+        lo[u] = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(hi_full);
+      if (!kSum && !mbar_wait_w(a_done, c & 1, env)) break;
+#pragma unroll
+      for (int u = 0; u < D1 / 8; ++u) *reinterpret_cast<uint4*>(tA + unit_offset(kChunk, j, u)) = lo[u];
+      fence_proxy_async_smem();
+      mbar_arrive(lo_full);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  // rows of out outside every sequence
+  if (!kSum && p.zero_outside) {
+    auto clear = [&](int t0, int t1) {
+      constexpr int kUnits = D2 / 8;
+      for (long long x = threadIdx.x; x < (long long)(t1 - t0) * kUnits; x += kThreads)
+        *reinterpret_cast<uint4*>(w.out + (t0 + x / kUnits) * w.out_stride + (long long)h * D2 + x % kUnits * 8) =
+            make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (f.seq == 0 && f.seg == 0) clear(0, f.s0);
+    if (f.seq == p.N - 1 && f.seg == f.n_seg - 1) clear(f.s1, p.T);
+  }
+}
+
+// DA, DB: the widths (d1, d2) of the walks; a `swapped` walk has them exchanged.
+template <int DA, int DB, bool kSum>
+__global__ void __launch_bounds__(kThreads, 1) decay_walk_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Found found;
+  const int wi = blockIdx.x % p.n_walks, h = blockIdx.x / p.n_walks % p.H, item = blockIdx.x / p.n_walks / p.H;
+  const WalkParams& w = p.w[wi];
+  if (threadIdx.x < 32) {
+    bool valid;
+    const Segment g = find_segment(p.cu, p.N, p.T, p.L, kSegments, item, threadIdx.x, valid);
+    const int row = !kSum && g.seq >= 0 && (w.init || w.fin)
+                        ? pool_row(p.slots, g.seq, p.n_slots, w.fin != nullptr, threadIdx.x, p.wc.status)
+                        : -1;
+    if (threadIdx.x == 0) {
+      if (!valid) report_status(p.wc.status, kStatusInvalidArg);
+      found = Found{g.seq, g.s0, g.s1, g.seg, g.n_seg, g.t0, g.t1, g.rec, row,
+                    g.seq >= 0 && (!p.resume || p.resume[g.seq]) ? 1 : 0};
+      prefetch_tmap(&w.a);
+      prefetch_tmap(&w.b);
+      prefetch_tmap(&w.c);
+    }
+  }
+  __syncthreads();
+  if (found.seq < 0) return;
+  // nothing enters a segment from the one walked last, and nothing is cut in an uncut sequence
+  if (kSum && (found.n_seg == 1 || found.seg == (w.reverse ? 0 : found.n_seg - 1))) return;
+  if constexpr (DA != DB) {
+    if (w.swapped) {
+      walk<DB, DA, kSum>(p, w, h, smem, found);
+      return;
+    }
+  }
+  walk<DA, DB, kSum>(p, w, h, smem, found);
+}
+
+// The sums of a split sequence's segments become the states that enter them:
+// E_first = init, E_next = a^(tokens) E + sum, in walking order.  One thread
+// per four values; the sums of up to kAhead segments are in flight at once.
+constexpr int kScanThreads = 256, kAhead = 8;
+
+__global__ void __launch_bounds__(kScanThreads) decay_scan_kernel(const __grid_constant__ Params p, int d_a, int d_b) {
+  __shared__ Found found;
+  const int part = d_a * d_b / 4 / kScanThreads, y = blockIdx.x / part;
+  const int wi = y % p.n_walks, h = y / p.n_walks % p.H, item = y / p.n_walks / p.H;
+  const WalkParams& w = p.w[wi];
+  if (threadIdx.x < 32) {
+    bool valid;
+    const Segment g = find_segment(p.cu, p.N, p.T, p.L, kSplitSequences, item, threadIdx.x, valid);
+    const int row = g.seq >= 0 && w.init
+                        ? pool_row(p.slots, g.seq, p.n_slots, w.fin != nullptr, threadIdx.x, p.wc.status)
+                        : -1;
+    if (threadIdx.x == 0)
+      found = Found{g.seq, g.s0, g.s1, g.seg, g.n_seg, g.t0, g.t1, g.rec, row,
+                    g.seq >= 0 && (!p.resume || p.resume[g.seq]) ? 1 : 0};
+  }
+  __syncthreads();
+  const Found f = found;
+  if (f.seq < 0) return;
+  const bool rev = w.reverse != 0;
+  const int d1 = w.swapped ? d_b : d_a, d2 = w.swapped ? d_a : d_b;
+  const int size4 = d1 * d2 / 4, x = blockIdx.x % part * kScanThreads + threadIdx.x;
+  const float g = used_log_decay(p.log_decay[h], p.wc.status);
+  float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (f.row >= 0 && f.resumed) {
+    const float* src = w.init + ((long long)f.row * p.H + h) * (4ll * size4);
+    if (w.init_transposed) {
+      const int r = 4 * x / d2, c = 4 * x % d2;
+      e = make_float4(src[c * d1 + r], src[(c + 1) * d1 + r], src[(c + 2) * d1 + r], src[(c + 3) * d1 + r]);
+    } else {
+      e = reinterpret_cast<const float4*>(src)[x];
+    }
+  }
+  griddep_wait();
+  auto at = [&](int s) {  // s-th segment walked
+    const int seg = rev ? f.n_seg - 1 - s : s;
+    return reinterpret_cast<float4*>(w.rec) + ((long long)(f.rec + seg) * p.H + h) * size4 + x;
+  };
+  auto factor = [&](int s) {
+    const int seg = rev ? f.n_seg - 1 - s : s;
+    return expf(g * (float)(min(p.L, f.s1 - f.s0 - seg * p.L)));
+  };
+  for (int s0 = 0; s0 < f.n_seg; s0 += kAhead) {
+    float4 sum[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (s0 + u < f.n_seg - 1) sum[u] = *at(s0 + u);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (s0 + u >= f.n_seg) break;
+      *at(s0 + u) = e;
+      if (s0 + u < f.n_seg - 1) {
+        const float k = factor(s0 + u);
+        e = make_float4(fmaf(k, e.x, sum[u].x), fmaf(k, e.y, sum[u].y), fmaf(k, e.z, sum[u].z),
+                        fmaf(k, e.w, sum[u].w));
+      }
+    }
+  }
+}
+
+// fin = init or zero, for sequences without tokens (T = 0)
+__global__ void __launch_bounds__(256) decay_empty_kernel(const float* init, float* fin, const int* slots, int n_slots,
+                                                          const unsigned char* resume, long long size4, int* status) {
+  const int n = blockIdx.x;
+  const int row = pool_row(slots, n, n_slots, true, threadIdx.x & 31, status);
+  const long long x = (long long)blockIdx.y * 256 + threadIdx.x;
+  if (row < 0 || x >= size4) return;
+  const bool entered = init && (!resume || resume[n]);
+  reinterpret_cast<float4*>(fin)[row * size4 + x] =
+      entered ? reinterpret_cast<const float4*>(init)[row * size4 + x] : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// [T][H][width] with `stride` elements between tokens, box [128 tokens][1 head][64 values], 128-byte swizzle
+bool make_tmap(CUtensorMap* map, const void* base, int width, int H, int T, long long stride) {
+  typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const EncodeFn enc = []() -> EncodeFn {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &qr) != cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeFn>(fn);
+  }();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, kChunk};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How sequences are cut.  The lengths are on the device; the plan knows T, N,
+// the heads and the walks, and takes the length of segments that would be
+// best for sequences of equal length: a CTA per segment, waves of 148, a
+// chunk as the unit, about two more for a CTA's start and end, and where
+// anything is cut half as much again for the sums and a few chunks' time for
+// two more launches.  Shorter segments than kMinSegment or twice an even
+// share of the work are not taken, so that a call whose sequences differ is
+// cut only where one of them would outlast the rest.
+struct Plan {
+  int L;              // tokens per segment, a multiple of 128
+  int max_segments;   // of all sequences together
+  int max_records;    // of split sequences
+};
+
+constexpr int kSMs = 148, kMinSegment = 8;
+
+Plan make_plan(int T, int H, int N, int walks) {
+  const long long heads = (long long)H * walks;
+  const long long len = ((long long)T / N + kChunk - 1) / kChunk;  // chunks of an even sequence
+  long long best = -1, k_best = 1;
+  for (long long k = std::max(len, 1ll); k >= 1; k = k > 64 ? k - k / 32 : k - 1) {
+    const long long segs = (std::max(len, 1ll) + k - 1) / k, waves = (segs * N * heads + kSMs - 1) / kSMs;
+    const long long cost = waves * (2 * k + 4) + (segs > 1 ? waves * k + 16 : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      k_best = k;
+    }
+  }
+  const long long chunks = ((long long)T + kChunk - 1) / kChunk;
+  const long long share = N > 1 ? 2 * ((chunks + N) * heads / kSMs) : 0;
+  const long long k = std::max(std::max(k_best, share), (long long)kMinSegment);
+  Plan pl;
+  pl.L = (int)std::min(k * kChunk, 1ll << 30);
+  pl.max_segments = N + T / pl.L;
+  pl.max_records = T > pl.L ? T / pl.L + std::min(N, T / pl.L) : 0;
+  return pl;
+}
+
+template <int DA, int DB>
+cudaError_t launch(const Params& p, const Plan& pl, cudaStream_t st) {
+  constexpr int bytes = Cfg<DA, DB>::kBytes > Cfg<DB, DA>::kBytes ? Cfg<DA, DB>::kBytes : Cfg<DB, DA>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(decay_walk_kernel<DA, DB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       bytes);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)pl.max_segments * p.H * p.n_walks);
+  if (pl.max_records == 0) {
+    decay_walk_kernel<DA, DB, false><<<grid, kThreads, bytes, st>>>(p);
+    return cudaGetLastError();
+  }
+  e = cudaFuncSetAttribute(decay_walk_kernel<DA, DB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  decay_walk_kernel<DA, DB, true><<<grid, kThreads, bytes, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const dim3 scan(DA * DB / 4 / kScanThreads * (unsigned)std::min(p.N, p.T / pl.L) * p.H * p.n_walks);
+  e = launch_pdl(decay_scan_kernel, scan, dim3(kScanThreads), 0, st, p, DA, DB);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decay_walk_kernel<DA, DB, false>, grid, dim3(kThreads), (size_t)bytes, st, p);
+}
+
+}  // namespace
+
+size_t decay_workspace_bytes(int T, int H, int d1, int d2, int N, int walks) {
+  return (size_t)walks * make_plan(T, H, N, walks).max_records * H * d1 * d2 * sizeof(float);
+}
+
+cudaError_t launch_decay_walks(const DecayWalk* walks, int n, const DecayShape& sh, void* ws, const WaitCtl& wc,
+                               cudaStream_t st) {
+  if (n < 1 || n > kMaxWalks) return cudaErrorInvalidValue;
+  const Plan pl = make_plan(sh.T, sh.H, sh.N, n);
+  Params p{};
+  const int da = walks[0].d1, db = walks[0].d2;
+  for (int i = 0; i < n; ++i) {
+    const DecayWalk& x = walks[i];
+    WalkParams& w = p.w[i];
+    if (!make_tmap(&w.a, x.a, x.d1, sh.H, sh.T, x.a_stride) || !make_tmap(&w.b, x.b, x.d1, sh.H, sh.T, x.b_stride) ||
+        !make_tmap(&w.c, x.c, x.d2, sh.H, sh.T, x.c_stride))
+      return cudaErrorInvalidValue;
+    w.out = static_cast<__nv_bfloat16*>(x.out);
+    w.out_stride = x.out_stride;
+    w.init = x.init;
+    w.fin = x.fin;
+    w.rec = static_cast<float*>(ws) + (size_t)i * pl.max_records * sh.H * x.d1 * x.d2;
+    w.swapped = x.d1 != da;
+    w.reverse = x.reverse;
+    w.init_transposed = x.init_transposed;
+    w.s_intra = sh.scale;
+    w.s_inter = x.reverse ? 1.f : sh.scale;
+    w.s_key = x.reverse ? sh.scale : 1.f;
+  }
+  p.cu = sh.cu;
+  p.log_decay = sh.log_decay;
+  p.slots = sh.slots;
+  p.resume = sh.resume;
+  p.n_walks = n;
+  p.T = sh.T;
+  p.H = sh.H;
+  p.N = sh.N;
+  p.L = pl.L;
+  p.n_slots = sh.n_slots;
+  p.zero_outside = sh.zero_outside;
+  p.wc = wc;
+  if (da == 64 && db == 64) return launch<64, 64>(p, pl, st);
+  if (da == 128 && db == 128) return launch<128, 128>(p, pl, st);
+  if (da == 64) return launch<64, 128>(p, pl, st);
+  return launch<128, 64>(p, pl, st);
+}
+
+cudaError_t launch_decay_empty(const DecayWalk& w, const DecayShape& sh, const WaitCtl& wc, cudaStream_t st) {
+  if (!w.fin) return cudaSuccess;
+  const long long size4 = (long long)sh.H * w.d1 * w.d2 / 4;
+  decay_empty_kernel<<<dim3((unsigned)sh.N, (unsigned)((size4 + 255) / 256)), 256, 0, st>>>(
+      w.init, w.fin, sh.slots, sh.n_slots, sh.resume, size4, wc.status);
+  return cudaGetLastError();
+}
+
+}  // namespace kata
