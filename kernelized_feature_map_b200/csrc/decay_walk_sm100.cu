@@ -22,13 +22,13 @@
 // reach only out, which is rounded as far itself.
 //
 // One CTA per segment of a sequence, head and walk (1 CTA per SM: 512 TMEM
-// columns).  Warps (576 threads):
+// columns).  Warps (640 threads):
 //   0       TMA: A, B, C tiles of the chunks into a ring of kStages
 //   1       TMEM allocator; MMA issue (whole warp, one elected lane)
-//   2-9     W from P (two warps per TMEM lane quarter, half of the columns
-//           each), and out from the two accumulators
-//   10-13   S: the bf16 copy for the next chunk, and its scaling in TMEM
-//   14-17   B: hi in place over the tile once P is done, lo over the A tile once
+//   4-7     W from P, a TMEM lane quarter each (as the next two roles)
+//   8-11    out from the two accumulators
+//   12-15   S: the bf16 copy for the next chunk, and its scaling in TMEM
+//   16-19   B: hi in place over the tile once P is done, lo over the A tile once
 //           A has met S; rows past the sequence's end cleared in B and C,
 //           so that nothing of the next sequence (NaN included) gets in
 // MMA order per chunk: P; A S; hi; W C; lo.  The state of the next chunk
@@ -58,7 +58,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 576;
+constexpr int kThreads = 512;  // at most 128 registers: more warps would spill, to L2, as shared memory leaves no L1
 constexpr int kMaxWalks = 3;
 constexpr uint32_t kTmemCols = 512;
 
@@ -95,8 +95,9 @@ struct Cfg {
   static constexpr int offCopy = kStages * kStage;
   static constexpr int offPow = offCopy + kCopy;        // a^0 .. a^128
   static constexpr int offCol = offPow + 132 * 4;       // column factors of a full 32-column block
-  static constexpr int offBar = offCol + 32 * 4;
-  static constexpr int kBars = 2 * kStages + 10;
+  static constexpr int offDiag = offCol + 32 * 4;       // s_intra a^|x| for x = -31 .. 31, from [1]
+  static constexpr int offBar = offDiag + 64 * 4;
+  static constexpr int kBars = 3 * kStages + 10;
   static constexpr int offMisc = offBar + kBars * 8;
   static constexpr int kBytes = offMisc + 64 + 1024;    // + alignment slack
   static constexpr uint32_t colP = 0, colI = 128, colE = 128 + D2, colS = 128 + 2 * D2;
@@ -114,25 +115,116 @@ __device__ __forceinline__ uint32_t unit_offset(int rows, int r, int u) {
   return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
 }
 
-template <int D1, int D2, bool kSum>
+// two values of a key times f1 + f2: returns the high parts, and the low ones in `lo`
+__device__ __forceinline__ uint32_t split_key(uint32_t k, __nv_bfloat162 f1, __nv_bfloat162 f2, uint32_t& lo) {
+  const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&k);
+  const __nv_bfloat162 hi = __hmul2(x, f1);
+  const __nv_bfloat162 l = __hfma2(x, f2, __hfma2(x, f1, __hneg2(hi)));
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  return *reinterpret_cast<const uint32_t*>(&hi);
+}
+
+__device__ __forceinline__ void store_32b(void* to, const uint32_t* z) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(z[0]), "r"(z[1]), "r"(z[2]),
+               "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
+               : "memory");
+}
+
+// Column and row of a lane: with d1 = 64 lanes 64-127 hold a second copy of the
+// state, and each half of the lanes handles one half of the columns in memory.
+template <int D1, int D2>
+struct StateLane {
+  int row, own0, own1;
+  __device__ __forceinline__ StateLane(int quarter, int lane)
+      : row((quarter * 32 + lane) % D1),
+        own0(D1 == 64 && quarter >= 2 ? D2 / 2 : 0),
+        own1(D1 == 64 && quarter < 2 ? D2 / 2 : D2) {}
+  __device__ __forceinline__ bool own(int b) const { return 32 * b >= own0 && 32 * b < own1; }
+};
+
+// the state in TMEM to [d1][d2] fp32
+template <int D1, int D2>
+__device__ __forceinline__ void write_state(uint32_t lane_base, const StateLane<D1, D2>& l, float* dst) {
+#pragma unroll 1
+  for (int b = 0; b < D2 / 32; ++b) {
+    uint32_t r[32];
+    tmem_ld32(lane_base + 32 * b, r);
+    tmem_wait_ld();
+    if (!l.own(b)) continue;
+    float4* d4 = reinterpret_cast<float4*>(dst + (long long)l.row * D2 + 32 * b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      d4[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                          __uint_as_float(r[4 * e + 3]));
+  }
+}
+
+// Key row j of a chunk of n tokens, scaled: hi in place in tB, lo returned.  The
+// factor is taken as f1 + f2 (error 2^-18): with hi = f1 k rounded, f1 k - hi is
+// a bf16 value, and lo is that and f2 k, rounded.  Rows past the end (another
+// sequence's, or nothing) are cleared, in tC too.
+template <int D1, int D2>
+__device__ __forceinline__ void scale_key_row(uint8_t* tB, uint8_t* tC, int j, int n, float fac,
+                                              uint32_t (&lo)[D1 / 2]) {
+  const __nv_bfloat16 f1 = __float2bfloat16_rn(fac), f2 = __float2bfloat16_rn(fac - __bfloat162float(f1));
+  const __nv_bfloat162 g1 = __halves2bfloat162(f1, f1), g2 = __halves2bfloat162(f2, f2);
+  if (j < n) {
+#pragma unroll
+    for (int u = 0; u < D1 / 8; ++u) {
+      uint4* at = reinterpret_cast<uint4*>(tB + unit_offset(kChunk, j, u));
+      const uint4 in = *at;
+      uint4 hi;
+      hi.x = split_key(in.x, g1, g2, lo[4 * u]);
+      hi.y = split_key(in.y, g1, g2, lo[4 * u + 1]);
+      hi.z = split_key(in.z, g1, g2, lo[4 * u + 2]);
+      hi.w = split_key(in.w, g1, g2, lo[4 * u + 3]);
+      *at = hi;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < D1 / 8; ++u) {
+      *reinterpret_cast<uint4*>(tB + unit_offset(kChunk, j, u)) = make_uint4(0u, 0u, 0u, 0u);
+      lo[4 * u] = lo[4 * u + 1] = lo[4 * u + 2] = lo[4 * u + 3] = 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < D2 / 8; ++u)
+      *reinterpret_cast<uint4*>(tC + unit_offset(kChunk, j, u)) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+template <int D1>
+__device__ __forceinline__ void write_low_row(uint8_t* tA, int j, const uint32_t (&lo)[D1 / 2]) {
+#pragma unroll
+  for (int u = 0; u < D1 / 8; ++u)
+    *reinterpret_cast<uint4*>(tA + unit_offset(kChunk, j, u)) =
+        make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+}
+
+// descriptors of the state's products: scaled keys (M-major), and the C tile (N-major)
+template <int D1>
+__device__ __forceinline__ uint64_t key_desc(uint32_t tile) {
+  return smem_desc(tile, D1 == 128 ? 16384u : 0u, 1024, kSw128);
+}
+
+template <int D1, int D2>
 __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem, const Found& f) {
   using C = Cfg<D1, D2>;
   constexpr int kStages = C::kStages;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::offBar);
   uint64_t* full = bars;               // [kStages] tiles landed
-  uint64_t* empty = full + kStages;    // [kStages] tiles read
-  uint64_t* p_full = empty + kStages;  // P in TMEM
-  uint64_t* w_full = p_full + 1;       // W written (256)
+  uint64_t* p_full = full + kStages;   // P in TMEM
+  uint64_t* w_full = p_full + 1;       // W written (128)
   uint64_t* s_ready = w_full + 1;      // S scaled and copied (128)
   uint64_t* a_done = s_ready + 1;      // A has met B and S: its tile takes lo
   uint64_t* hi_full = a_done + 1;      // hi written, rows past the end cleared (128)
   uint64_t* lo_full = hi_full + 1;     // lo written (128)
   uint64_t* o_full = lo_full + 1;      // both accumulators of out complete
-  uint64_t* o_free = o_full + 1;       // and read (256)
-  uint64_t* s_done = o_free + 1;       // S advanced
+  uint64_t* o_free = o_full + 1;       // and read (128)
+  uint64_t* s_done = o_free + 1;       // S advanced; the chunk's tiles are free
   uint64_t* mma_done = s_done + 1;     // every MMA issued has completed
   float* pw = reinterpret_cast<float*>(smem + C::offPow);
   float* col = reinterpret_cast<float*>(smem + C::offCol);
+  float* diag = reinterpret_cast<float*>(smem + C::offDiag);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offMisc + 4);
 
@@ -142,24 +234,36 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   // c-th chunk walked: its first token and its tokens
   auto chunk_t = [&](int c) { return f.t0 + (rev ? n_chunks - 1 - c : c) * kChunk; };
   auto chunk_n = [&](int c) { return min(kChunk, f.t1 - chunk_t(c)); };
+  // tiles of a chunk (one thread)
+  auto load = [&](int c) {
+    const int st = c % kStages, t = chunk_t(c);
+    uint8_t* base = smem + C::offStage + st * C::kStage;
+    mbar_arrive_expect_tx(full + st, C::kStage);
+#pragma unroll
+    for (int x = 0; x < D1 / 64; ++x) {
+      tma_load_3d(base + x * 16384, &w.a, full + st, 64 * x, h, t);
+      tma_load_3d(base + C::kA + x * 16384, &w.b, full + st, 64 * x, h, t);
+    }
+#pragma unroll
+    for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + 2 * C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
+  };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 1);
-    }
+    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1);
     mbar_init(p_full, 1);
-    mbar_init(w_full, 256);
+    mbar_init(w_full, 128);
     mbar_init(s_ready, 128);
     mbar_init(a_done, 1);
     mbar_init(hi_full, 128);
     mbar_init(lo_full, 128);
     mbar_init(o_full, 1);
-    mbar_init(o_free, 256);
+    mbar_init(o_free, 128);
     mbar_init(s_done, 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    fence_proxy_async_smem();
+    for (int c = 0; c < min(kStages, n_chunks); ++c) load(c);
   }
   const float g = used_log_decay(p.log_decay[h], p.wc.status);
   if (threadIdx.x >= 64 && threadIdx.x < 64 + 129) pw[threadIdx.x - 64] = expf(g * (float)(threadIdx.x - 64));
@@ -167,6 +271,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     const int j = threadIdx.x - 224;
     col[j] = expf(g * (float)(rev ? j : 31 - j));
   }
+  if (threadIdx.x >= 256 && threadIdx.x < 256 + 64)
+    diag[threadIdx.x - 256] = w.s_intra * expf(g * fabsf((float)((int)threadIdx.x - 256 - 32)));
   if (warp == 1) tmem_alloc(tmem_holder, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -174,47 +280,65 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   const uint32_t tmem = *tmem_holder;
   const WaitEnv env{p.wc.status, abort_flag, p.wc.limit};
 
-  if (warp == 0) {
-    // --------------------------------------------------------------- TMA
-    if (lane == 0) {
-      int issued = 0;
-      for (int c = 0; c < n_chunks; ++c) {
-        const int st = c % kStages;
-        if (!mbar_wait(empty + st, ((c / kStages) & 1) ^ 1, env)) break;
-        uint8_t* base = smem + C::offStage + st * C::kStage;
-        const int t = chunk_t(c);
-        mbar_arrive_expect_tx(full + st, kSum ? C::kA + C::kC : C::kStage);
-#pragma unroll
-        for (int x = 0; x < D1 / 64; ++x) {
-          if (!kSum) tma_load_3d(base + x * 16384, &w.a, full + st, 64 * x, h, t);
-          tma_load_3d(base + C::kA + x * 16384, &w.b, full + st, 64 * x, h, t);
-        }
-#pragma unroll
-        for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + 2 * C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
-        ++issued;
-      }
-      // every copy this CTA started must land before it exits
-      for (int c = issued - kStages < 0 ? 0 : issued - kStages; c < issued; ++c)
-        mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
+  if (warp < 4) {
+    // --------------------------------------------------------------- S; warp 0: every copy and MMA
+    const int quarter = warp;
+    const StateLane<D1, D2> l(quarter, lane);
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colS;
+    uint8_t* copy = smem + C::offCopy;
+    const long long size = (long long)D1 * D2;
+    const bool split = f.n_seg > 1;
+    const float* src = nullptr;
+    bool transposed = false;
+    if (split) {
+      src = w.rec + ((long long)(f.rec + f.seg) * p.H + h) * size;
+    } else if (w.init && f.row >= 0 && f.resumed) {
+      src = w.init + ((long long)f.row * p.H + h) * size;
+      transposed = w.init_transposed != 0;
     }
-  } else if (warp == 1) {
-    // --------------------------------------------------------------- MMA
+    float* dst = w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1)
+                     ? w.fin + ((long long)f.row * p.H + h) * size
+                     : nullptr;
+    // a block of 32 columns of the state before a chunk: its copy, and itself scaled
+    auto put = [&](int b, const uint32_t (&r)[32], uint64_t keep) {
+      if (l.own(b)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t z[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
+          *reinterpret_cast<uint4*>(copy + unit_offset(D1, l.row, 4 * b + e)) = make_uint4(z[0], z[1], z[2], z[3]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint32_t z[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint64_t v = f32x2_mul(f32x2(r[16 * s + 2 * e], r[16 * s + 2 * e + 1]), keep);
+          z[2 * e] = (uint32_t)v;
+          z[2 * e + 1] = (uint32_t)(v >> 32);
+        }
+        tmem_st16(lane_base + 32 * b + 16 * s, z);
+      }
+    };
     constexpr uint32_t id_p = idesc_bf16(128, 128, false, false);  // A, B both K-major
     constexpr uint32_t id_o = idesc_bf16(128, D2, false, true);    // A or W, and C or the copy of S (N-major)
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);     // B^T (M-major), C (N-major)
-    constexpr uint32_t kAtom = D1 == 128 ? 16384u : 0u;            // second 64 rows of the state: see above
-    const uint32_t sStage = smem_u32(smem + C::offStage), sCopy = smem_u32(smem + C::offCopy);
-    const uint64_t dcopy = smem_desc(sCopy, D1 * 128, 1024, kSw128);
+    const uint32_t sStage = smem_u32(smem + C::offStage);
+    const uint64_t dcopy = smem_desc(smem_u32(copy), D1 * 128, 1024, kSw128);
+    int loaded = min(kStages, n_chunks);
+    if (split) griddep_wait();  // the scan's states
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
       const uint32_t sA = sStage + st * C::kStage, sB = sA + C::kA, sC = sB + C::kA;
-      const uint64_t dA = smem_desc(sA, 16, 1024, kSw128), dB = smem_desc(sB, 16, 1024, kSw128);
-      const uint64_t dC = smem_desc(sC, 16384, 1024, kSw128);
-      const uint64_t dHi = smem_desc(sB, kAtom, 1024, kSw128), dLo = smem_desc(sA, kAtom, 1024, kSw128);
-      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
-      tc_fence_after();
-      if (!kSum) {
-        // over W of the chunk before only after its products, issued before
+      const uint64_t dA = smem_desc(sA, 16, 1024, kSw128), dC = smem_desc(sC, 16384, 1024, kSw128);
+      if (warp == 0) {
+        if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
+        tc_fence_after();
+        const uint64_t dB = smem_desc(sB, 16, 1024, kSw128);
+        // over W of the chunk before only after its product, which was issued before
 #pragma unroll
         for (int ks = 0; ks < D1 / 16; ++ks) {
           const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
@@ -222,268 +346,211 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
         }
         mma_commit_w(p_full);
       }
-      if (!mbar_wait_w(s_ready, c & 1, env)) break;
-      if (!kSum) {
-        if (c > 0 && !mbar_wait_w(o_free, (c - 1) & 1, env)) break;
-        tc_fence_after();
+      const uint32_t kf = __float_as_uint(pw[chunk_n(c)]);
+      const uint64_t keep = f32x2(kf, kf);
+      if (c == 0) {
+#pragma unroll 1
+        for (int b = 0; b < D2 / 32; ++b) {
+          uint32_t r[32];
+          if (src && !transposed) {
+            const float4* s4 = reinterpret_cast<const float4*>(src + (long long)l.row * D2 + 32 * b);
 #pragma unroll
-        for (int ks = 0; ks < D1 / 16; ++ks)
-          mma_ss_w(tmem + C::colE, desc_add(dA, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dcopy, ks * 2048), id_o,
-                   ks > 0);
-        mma_commit_w(a_done);
+            for (int e = 0; e < 8; ++e) {
+              const float4 x = s4[e];
+              r[4 * e] = __float_as_uint(x.x);
+              r[4 * e + 1] = __float_as_uint(x.y);
+              r[4 * e + 2] = __float_as_uint(x.z);
+              r[4 * e + 3] = __float_as_uint(x.w);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              r[e] = src ? __float_as_uint(src[(long long)(32 * b + e) * D1 + l.row]) : 0u;
+          }
+          put(b, r, keep);
+        }
+      } else {
+        if (!mbar_wait_w(s_done, (c - 1) & 1, env)) break;
+        tc_fence_after();
+        if (warp == 0 && loaded < n_chunks) {  // into the tiles of the chunk before
+          if (lane == 0) load(loaded);
+          ++loaded;
+          __syncwarp();
+        }
+        // two blocks of 32 columns in flight
+#pragma unroll 1
+        for (int b = 0; b < D2 / 32; b += 2) {
+          uint32_t r0[32], r1[32];
+          tmem_ld32(lane_base + 32 * b, r0);
+          tmem_ld32(lane_base + 32 * b + 32, r1);
+          tmem_wait_ld();
+          put(b, r0, keep);
+          put(b + 1, r1, keep);
+        }
       }
+      tmem_wait_st();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(s_ready);
+      if (warp != 0) continue;
+      if (!mbar_wait_w(s_ready, c & 1, env)) break;
+      if (c > 0 && !mbar_wait_w(o_free, (c - 1) & 1, env)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < D1 / 16; ++ks)
+        mma_ss_w(tmem + C::colE, desc_add(dA, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dcopy, ks * 2048), id_o,
+                 ks > 0);
+      mma_commit_w(a_done);
       if (!mbar_wait_w(hi_full, c & 1, env)) break;
       tc_fence_after();
+      const uint64_t dHi = key_desc<D1>(sB), dLo = key_desc<D1>(sA);
 #pragma unroll
       for (int ks = 0; ks < kChunk / 16; ++ks)
         mma_ss_w(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
-      if (!kSum) {
-        if (!mbar_wait_w(w_full, c & 1, env)) break;
-        tc_fence_after();
+      if (!mbar_wait_w(w_full, c & 1, env)) break;
+      tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < kChunk / 16; ++ks)  // keys 16 ks ..: W columns 64 (ks / 4) + 8 (ks % 4)
-          mma_ts_w(tmem + C::colI, tmem + C::colP + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(dC, ks * 2048), id_o,
-                   ks > 0);
-        mma_commit_w(o_full);
-      }
+      for (int ks = 0; ks < kChunk / 16; ++ks)  // keys 16 ks ..: W columns 8 ks ..
+        mma_ts_w(tmem + C::colI, tmem + C::colP + ks * 8, desc_add(dC, ks * 2048), id_o, ks > 0);
+      mma_commit_w(o_full);
       if (!mbar_wait_w(lo_full, c & 1, env)) break;
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < kChunk / 16; ++ks)
         mma_ss_w(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
       mma_commit_w(s_done);
-      mma_commit_w(empty + st);
     }
-    mma_commit_w(mma_done);
-    mbar_wait_drain(mma_done, 0);
-  } else if (warp < 10) {
-    // --------------------------------------------------------------- W and out
-    const int quarter = warp % 4, half = warp >= 6 ? 1 : 0;
-    const int i = quarter * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    // a^(i-j) = a^(i-j1) a^(j1-j) for the columns j0 .. j1 = j0 + 31 of a block
-    // left of the diagonal, both exponents >= 0; backwards a^(j-i) =
-    // a^(j0-i) a^(j-j0) right of it: a factor of the row, constant over the
-    // chunks, and one of the column, the same for all blocks
-    float row_f[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int j0 = 32 * (2 * half + b), e = rev ? j0 - i : i - j0 - 31;
-      row_f[b] = e >= 0 ? pw[e] : 0.f;
+    if (n_chunks > 0) {
+      if (mbar_wait_w(s_done, (n_chunks - 1) & 1, env) && dst) {
+        tc_fence_after();
+        write_state(lane_base, l, dst);
+      }
+    } else if (dst) {  // an empty sequence leaves what it starts from
+      for (int j = l.own0; j < l.own1; ++j)
+        dst[(long long)l.row * D2 + j] =
+            src ? src[transposed ? (long long)j * D1 + l.row : (long long)l.row * D2 + j] : 0.f;
     }
-    const float reach_f = pw[i + 1];
-    for (int c = 0; !kSum && c < n_chunks; ++c) {
+    if (!split) griddep_wait();  // a grid ends after those it was launched behind
+    if (warp == 0) {
+      // every MMA and copy that was issued ends before the CTA does
+      mma_commit_w(mma_done);
+      mbar_wait_drain(mma_done, 0);
+      for (int c = max(loaded - kStages, 0); c < loaded; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
+    }
+  } else if (warp < 8) {
+    // --------------------------------------------------------------- W
+    const int quarter = warp % 4, i = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colP;
+    // Left of the diagonal, for the columns j0 .. j1 = j0 + 31 of a block,
+    // a^(i-j) = a^(i-j1) a^(j1-j), both exponents >= 0; backwards a^(j-i) =
+    // a^(j0-i) a^(j-j0) right of it: a factor of the row and one of the
+    // column, the same for all blocks.
+    for (int c = 0; c < n_chunks; ++c) {
       const int n = chunk_n(c);
       if (!mbar_wait_w(p_full, c & 1, env)) break;
       tc_fence_after();
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int bb = 2 * half + b;
+      for (int bb = 0; bb < 4; ++bb) {
         uint32_t x[16];
         if (rev ? bb < quarter : bb > quarter) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = 0u;
         } else {
           uint32_t r[32];
-          tmem_ld32(lane_base + C::colP + 32 * bb, r);
+          tmem_ld32(lane_base + 32 * bb, r);
           tmem_wait_ld();
           if (bb != quarter) {
-            const uint64_t rf = f32x2(__float_as_uint(row_f[b]), __float_as_uint(row_f[b]));
+            const uint32_t f = __float_as_uint(w.s_intra * pw[rev ? 32 * bb - i : i - 32 * bb - 31]);
+            const uint64_t rf = f32x2(f, f);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float4 cf = reinterpret_cast<const float4*>(col)[e / 2];
-              const uint64_t lo = f32x2_mul(f32x2_mul(f32x2(r[2 * e], r[2 * e + 1]), rf),
-                                            f32x2(__float_as_uint(cf.x), __float_as_uint(cf.y)));
-              const uint64_t hi = f32x2_mul(f32x2_mul(f32x2(r[2 * e + 2], r[2 * e + 3]), rf),
-                                            f32x2(__float_as_uint(cf.z), __float_as_uint(cf.w)));
+              const ulonglong2 cf = reinterpret_cast<const ulonglong2*>(col)[e / 2];
+              const uint64_t lo = f32x2_mul(f32x2_mul(f32x2(r[2 * e], r[2 * e + 1]), rf), cf.x);
+              const uint64_t hi = f32x2_mul(f32x2_mul(f32x2(r[2 * e + 2], r[2 * e + 3]), rf), cf.y);
               x[e] = pack_bf16x2(f32x2_lo(lo), f32x2_hi(lo));
               x[e + 1] = pack_bf16x2(f32x2_lo(hi), f32x2_hi(hi));
             }
-            if (rev && 32 * bb + 32 > n) {  // columns past the end hold another sequence's rows
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int j = 32 * bb + 2 * e;
-                x[e] = j >= n ? 0u : j + 1 >= n ? x[e] & 0xffffu : x[e];
-              }
-            }
           } else {
+            // the table holds s_intra a^|i-j|; what stands beyond the diagonal is cut off below
+            const float* t = diag + (rev ? 32 - lane : 32 + lane);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float v[2];
+              const float w0 = rev ? t[2 * e] : t[-2 * e], w1 = rev ? t[2 * e + 1] : t[-2 * e - 1];
+              const uint32_t y = pack_bf16x2(__uint_as_float(r[2 * e]) * w0, __uint_as_float(r[2 * e + 1]) * w1);
+              const bool k0 = rev ? 2 * e >= lane : 2 * e <= lane, k1 = rev ? 2 * e + 1 >= lane : 2 * e + 1 <= lane;
+              x[e] = y & ((k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u));
+            }
+          }
+          if (rev && 32 * bb + 32 > n) {  // columns past the end hold another sequence's rows
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int jj = 2 * e + y, away = rev ? jj - lane : lane - jj;
-                const bool keep = away >= 0 && (!rev || 32 * bb + jj < n);
-                v[y] = keep ? __uint_as_float(r[jj]) * pw[keep ? away : 0] : 0.f;
-              }
-              x[e] = pack_bf16x2(v[0], v[1]);
+            for (int e = 0; e < 16; ++e) {
+              const int j = 32 * bb + 2 * e;
+              x[e] = j >= n ? 0u : j + 1 >= n ? x[e] & 0xffffu : x[e];
             }
           }
         }
-        tmem_st16(lane_base + C::colP + 64 * half + 16 * b, x);
+        tmem_st16(lane_base + 16 * bb, x);
       }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(w_full);
-      // out = s_intra W C + s_inter a^reach A S
+    }
+  } else if (warp < 12) {
+    // --------------------------------------------------------------- out = W C + s_inter a^reach A S
+    const int quarter = warp % 4, i = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    // stores of 32 bytes, where every row starts on such a boundary
+    const bool wide = ((reinterpret_cast<uintptr_t>(w.out) | (uintptr_t)(w.out_stride * 2)) & 31) == 0;
+    for (int c = 0; c < n_chunks; ++c) {
+      const int n = chunk_n(c);
+      const uint32_t f = __float_as_uint(w.s_inter * pw[rev ? max(n - 1 - i, 0) : i + 1]);
+      const uint64_t reach = f32x2(f, f);
+      __nv_bfloat16* orow = w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2;
       if (!mbar_wait_w(o_full, c & 1, env)) break;
       tc_fence_after();
-      const float reach = w.s_inter * (rev ? pw[max(n - 1 - i, 0)] : reach_f);
-      __nv_bfloat16* orow = w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + half * (D2 / 2);
 #pragma unroll
-      for (int b = 0; b < D2 / 64; ++b) {
-        uint32_t x[32], y[32];
-        tmem_ld32(lane_base + C::colI + half * (D2 / 2) + 32 * b, x);
-        tmem_ld32(lane_base + C::colE + half * (D2 / 2) + 32 * b, y);
+      for (int b = 0; b < D2 / 32; ++b) {
+        uint32_t x[32], y[32], z[16];
+        tmem_ld32(lane_base + C::colI + 32 * b, x);
+        tmem_ld32(lane_base + C::colE + 32 * b, y);
         tmem_wait_ld();
-        if (b == D2 / 64 - 1) {
+        if (b == D2 / 32 - 1) {
           tc_fence_before();
           mbar_arrive(o_free);
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t v = f32x2_fma(reach, f32x2(y[2 * e], y[2 * e + 1]), f32x2(x[2 * e], x[2 * e + 1]));
+          z[e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
+        }
         if (i < n) {
+          if (wide) {
+            store_32b(orow + 32 * b, z);
+            store_32b(orow + 32 * b + 16, z + 8);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t z[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              z[k] = pack_bf16x2(
-                  fmaf(reach, __uint_as_float(y[e + 2 * k]), w.s_intra * __uint_as_float(x[e + 2 * k])),
-                  fmaf(reach, __uint_as_float(y[e + 2 * k + 1]), w.s_intra * __uint_as_float(x[e + 2 * k + 1])));
-            *reinterpret_cast<uint4*>(orow + 32 * b + e) = make_uint4(z[0], z[1], z[2], z[3]);
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(orow + 32 * b + 8 * e) =
+                  make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
           }
         }
       }
-    }
-  } else if (warp < 14) {
-    // --------------------------------------------------------------- S
-    const int quarter = warp % 4;
-    const int m = quarter * 32 + lane, row = m % D1;
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colS;
-    uint8_t* copy = smem + C::offCopy;
-    // columns of the row that this warp writes out (d1 = 64: each half of the lanes one half)
-    const int own0 = D1 == 64 && quarter >= 2 ? D2 / 2 : 0, own1 = D1 == 64 && quarter < 2 ? D2 / 2 : D2;
-    const long long size = (long long)D1 * D2;
-    const bool split = f.n_seg > 1;
-    const float* src = nullptr;
-    bool transposed = false;
-    if (!kSum) {
-      griddep_wait();  // the segments' entering states (launched behind the scan, or behind nothing of this call)
-      if (split) {
-        src = w.rec + ((long long)(f.rec + f.seg) * p.H + h) * size;
-      } else if (w.init && f.row >= 0 && f.resumed) {
-        src = w.init + ((long long)f.row * p.H + h) * size;
-        transposed = w.init_transposed != 0;
-      }
-    }
-    float* dst = nullptr;
-    if (kSum)
-      dst = w.rec + ((long long)(f.rec + f.seg) * p.H + h) * size;
-    else if (w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1))
-      dst = w.fin + ((long long)f.row * p.H + h) * size;
-    if (n_chunks == 0 && dst) {  // an empty sequence leaves what it starts from
-      for (int j = own0; j < own1; ++j)
-        dst[(long long)row * D2 + j] = src ? src[transposed ? (long long)j * D1 + row : (long long)row * D2 + j] : 0.f;
-    }
-    for (int c = 0; c <= n_chunks && n_chunks > 0; ++c) {
-      // c = 0: the entering state; then the state after chunk c - 1
-      if (c > 0) {
-        if (!mbar_wait_w(s_done, (c - 1) & 1, env)) break;
-        tc_fence_after();
-      }
-      const float keep = c < n_chunks ? pw[chunk_n(c)] : 0.f;
-#pragma unroll 1
-      for (int b = 0; b < D2 / 32; ++b) {
-        uint32_t r[32];
-        if (c > 0) {
-          tmem_ld32(lane_base + 32 * b, r);
-          tmem_wait_ld();
-        } else if (src && !transposed) {
-          const float4* s4 = reinterpret_cast<const float4*>(src + (long long)row * D2 + 32 * b);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 x = s4[e];
-            r[4 * e] = __float_as_uint(x.x);
-            r[4 * e + 1] = __float_as_uint(x.y);
-            r[4 * e + 2] = __float_as_uint(x.z);
-            r[4 * e + 3] = __float_as_uint(x.w);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            r[e] = src ? __float_as_uint(src[(long long)(32 * b + e) * D1 + row]) : 0u;
-        }
-        const bool own = 32 * b >= own0 && 32 * b < own1;
-        if (c == n_chunks) {
-          if (dst && own) {
-            float4* d4 = reinterpret_cast<float4*>(dst + (long long)row * D2 + 32 * b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              d4[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                  __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-          }
-          continue;
-        }
-        if (!kSum && own) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t z[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
-            *reinterpret_cast<uint4*>(copy + unit_offset(D1, row, 4 * b + e)) = make_uint4(z[0], z[1], z[2], z[3]);
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          uint32_t z[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(keep * __uint_as_float(r[16 * s + e]));
-          tmem_st16(lane_base + 32 * b + 16 * s, z);
-        }
-      }
-      if (c == n_chunks) break;
-      tmem_wait_st();
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(s_ready);
     }
   } else {
     // --------------------------------------------------------------- B
-    const int j = (warp - 14) * 32 + lane;  // token of the chunk
+    const int j = (warp - 12) * 32 + lane;  // token of the chunk
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages, n = chunk_n(c);
       uint8_t* tA = smem + C::offStage + st * C::kStage;
-      uint8_t *tB = tA + C::kA, *tC = tB + C::kA;
       const float fac = j < n ? w.s_key * (rev ? pw[j + 1] : pw[n - 1 - j]) : 0.f;
       if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
-      if (!kSum && !mbar_wait_w(p_full, c & 1, env)) break;
-      if (j >= n) {
-#pragma unroll
-        for (int u = 0; u < D2 / 8; ++u)
-          *reinterpret_cast<uint4*>(tC + unit_offset(kChunk, j, u)) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      uint4 lo[D1 / 8];
-#pragma unroll
-      for (int u = 0; u < D1 / 8; ++u) {
-        uint4* at = reinterpret_cast<uint4*>(tB + unit_offset(kChunk, j, u));
-        const uint4 x = *at;
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        uint32_t h4[4], l4[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float a0 = fac * __uint_as_float(in[k] << 16), a1 = fac * __uint_as_float(in[k] & 0xffff0000u);
-          if (j >= n) a0 = a1 = 0.f;
-          h4[k] = pack_bf16x2(a0, a1);
-          l4[k] = pack_bf16x2(a0 - __uint_as_float(h4[k] << 16), a1 - __uint_as_float(h4[k] & 0xffff0000u));
-        }
-        *at = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-        lo[u] = make_uint4(l4[0], l4[1], l4[2], l4[3]);
-      }
+      if (!mbar_wait_w(p_full, c & 1, env)) break;
+      uint32_t lo[D1 / 2];
+      scale_key_row<D1, D2>(tA + C::kA, tA + 2 * C::kA, j, n, fac, lo);
       fence_proxy_async_smem();
       mbar_arrive(hi_full);
-      if (!kSum && !mbar_wait_w(a_done, c & 1, env)) break;
-#pragma unroll
-      for (int u = 0; u < D1 / 8; ++u) *reinterpret_cast<uint4*>(tA + unit_offset(kChunk, j, u)) = lo[u];
+      if (!mbar_wait_w(a_done, c & 1, env)) break;
+      write_low_row<D1>(tA, j, lo);
       fence_proxy_async_smem();
       mbar_arrive(lo_full);
     }
@@ -496,7 +563,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     tmem_dealloc(tmem, kTmemCols);
   }
   // rows of out outside every sequence
-  if (!kSum && p.zero_outside) {
+  if (p.zero_outside) {
     auto clear = [&](int t0, int t1) {
       constexpr int kUnits = D2 / 8;
       for (long long x = threadIdx.x; x < (long long)(t1 - t0) * kUnits; x += kThreads)
@@ -508,12 +575,116 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   }
 }
 
+// The sum of one segment of a sequence that is cut, from a zero state:
+//   sum_t a^(tokens of the segment after t) B_t C_t^T   (backwards: a^(tokens before t, and t))
+// With each key scaled for the segment's end nothing is carried from chunk to
+// chunk, so no product waits for another: bound by the loads of B and C.
+// Warps: 0 MMA, 1 TMA, 4-15 scale the keys in three groups, a chunk each.
+template <int D1, int D2>
+__device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t* smem, const Found& f) {
+  using C = Cfg<D1, D2>;
+  constexpr int kStages = C::kStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::offBar);  // [kStages] tiles landed
+  uint64_t* empty = full + kStages;                                // [kStages] tiles read
+  uint64_t* scaled = empty + kStages;                              // [kStages] hi and lo written (128)
+  uint64_t* mma_done = scaled + kStages;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::offMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+      mbar_init(scaled + s, 128);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  const float g = used_log_decay(p.log_decay[h], p.wc.status);
+  if (warp == 1) tmem_alloc(tmem_holder, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const WaitEnv env{p.wc.status, abort_flag, p.wc.limit};
+  if (warp == 0) {
+    constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);
+    const uint32_t sStage = smem_u32(smem + C::offStage);
+    for (int c = 0; c < n_chunks; ++c) {
+      const int st = c % kStages;
+      const uint32_t sA = sStage + st * C::kStage;
+      const uint64_t dLo = key_desc<D1>(sA), dHi = key_desc<D1>(sA + C::kA);
+      const uint64_t dC = smem_desc(sA + 2 * C::kA, 16384, 1024, kSw128);
+      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
+      if (!mbar_wait_w(scaled + st, (c / kStages) & 1, env)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < kChunk / 16; ++ks)
+        mma_ss_w(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, c > 0 || ks > 0);
+#pragma unroll
+      for (int ks = 0; ks < kChunk / 16; ++ks)
+        mma_ss_w(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+      mma_commit_w(empty + st);
+    }
+    mma_commit_w(mma_done);
+    mbar_wait_drain(mma_done, 0);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int c = 0; c < n_chunks; ++c) {
+        const int st = c % kStages, t = f.t0 + c * kChunk;
+        if (!mbar_wait(empty + st, ((c / kStages) & 1) ^ 1, env)) break;
+        uint8_t* base = smem + C::offStage + st * C::kStage + C::kA;
+        mbar_arrive_expect_tx(full + st, C::kA + C::kC);
+#pragma unroll
+        for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + x * 16384, &w.b, full + st, 64 * x, h, t);
+#pragma unroll
+        for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
+        ++issued;
+      }
+      // every copy that was issued ends before the CTA does
+      for (int c = max(issued - kStages, 0); c < issued; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int j = (warp & 3) * 32 + lane;  // token of the chunk
+    for (int c = (warp >> 2) - 1; c < n_chunks; c += 3) {
+      const int st = c % kStages, t = f.t0 + c * kChunk, n = min(kChunk, f.t1 - t);
+      uint8_t* tA = smem + C::offStage + st * C::kStage;
+      const float fac =
+          j < n ? w.s_key * expf(g * (float)(w.reverse ? t + j + 1 - f.t0 : f.t1 - 1 - t - j)) : 0.f;
+      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
+      uint32_t lo[D1 / 2];
+      scale_key_row<D1, D2>(tA + C::kA, tA + 2 * C::kA, j, n, fac, lo);
+      write_low_row<D1>(tA, j, lo);
+      fence_proxy_async_smem();
+      mbar_arrive(scaled + st);
+    }
+  }
+  if (warp < 4) {
+    if (mbar_wait_w(mma_done, 0, env)) {
+      tc_fence_after();
+      write_state(tmem + ((uint32_t)(warp * 32) << 16) + C::colS, StateLane<D1, D2>(warp, lane),
+                  w.rec + ((long long)(f.rec + f.seg) * p.H + h) * (D1 * D2));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
 // DA, DB: the widths (d1, d2) of the walks; a `swapped` walk has them exchanged.
 template <int DA, int DB, bool kSum>
 __global__ void __launch_bounds__(kThreads, 1) decay_walk_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Found found;
+  if constexpr (kSum) griddep_launch_dependents();
   const int wi = blockIdx.x % p.n_walks, h = blockIdx.x / p.n_walks % p.H, item = blockIdx.x / p.n_walks / p.H;
   const WalkParams& w = p.w[wi];
   if (threadIdx.x < 32) {
@@ -537,11 +708,17 @@ __global__ void __launch_bounds__(kThreads, 1) decay_walk_kernel(const __grid_co
   if (kSum && (found.n_seg == 1 || found.seg == (w.reverse ? 0 : found.n_seg - 1))) return;
   if constexpr (DA != DB) {
     if (w.swapped) {
-      walk<DB, DA, kSum>(p, w, h, smem, found);
+      if constexpr (kSum)
+        sum_segment<DB, DA>(p, w, h, smem, found);
+      else
+        walk<DB, DA>(p, w, h, smem, found);
       return;
     }
   }
-  walk<DA, DB, kSum>(p, w, h, smem, found);
+  if constexpr (kSum)
+    sum_segment<DA, DB>(p, w, h, smem, found);
+  else
+    walk<DA, DB>(p, w, h, smem, found);
 }
 
 // The sums of a split sequence's segments become the states that enter them:
@@ -551,6 +728,7 @@ constexpr int kScanThreads = 256, kAhead = 8;
 
 __global__ void __launch_bounds__(kScanThreads) decay_scan_kernel(const __grid_constant__ Params p, int d_a, int d_b) {
   __shared__ Found found;
+  griddep_launch_dependents();
   const int part = d_a * d_b / 4 / kScanThreads, y = blockIdx.x / part;
   const int wi = y % p.n_walks, h = y / p.n_walks % p.H, item = y / p.n_walks / p.H;
   const WalkParams& w = p.w[wi];
