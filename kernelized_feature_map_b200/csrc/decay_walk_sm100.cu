@@ -58,12 +58,12 @@ namespace {
 using namespace sm100;
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 512;  // at most 128 registers: more warps would spill, to L2, as shared memory leaves no L1
+constexpr int kThreads = 704;  // at most 128 registers: more warps would spill, to L2, as shared memory leaves no L1
 constexpr int kMaxWalks = 3;
 constexpr uint32_t kTmemCols = 512;
 
 struct WalkParams {
-  CUtensorMap a, b, c;
+  CUtensorMap a, b, c, o;
   __nv_bfloat16* out;
   long long out_stride;
   const float* init;
@@ -88,6 +88,8 @@ template <int D1, int D2>
 struct Cfg {
   static constexpr int kA = kChunk * D1 * 2, kC = kChunk * D2 * 2;  // tile bytes
   static constexpr int kStage = 2 * kA + kC;                         // [A | B | C]
+  // out leaves through the chunk's A tile, and where that is too small its B tile as well
+  static constexpr bool kLateB = kC > kA;
   static constexpr int kCopy = D1 * D2 * 2;
   static constexpr int kFit = (226 * 1024 - kCopy) / kStage;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;                // 2 (128, 128) .. 4 (64, 64)
@@ -97,7 +99,7 @@ struct Cfg {
   static constexpr int offCol = offPow + 132 * 4;       // column factors of a full 32-column block
   static constexpr int offDiag = offCol + 32 * 4;       // s_intra a^|x| for x = -31 .. 31, from [1]
   static constexpr int offBar = offDiag + 64 * 4;
-  static constexpr int kBars = 3 * kStages + 10;
+  static constexpr int kBars = 3 * kStages + 11;
   static constexpr int offMisc = offBar + kBars * 8;
   static constexpr int kBytes = offMisc + 64 + 1024;    // + alignment slack
   static constexpr uint32_t colP = 0, colI = 128, colE = 128 + D2, colS = 128 + 2 * D2;
@@ -113,21 +115,6 @@ struct Found {
 // 16-byte unit u (8 values) of row r in a tile of 128-byte swizzled rows, `rows` to a 64-column atom
 __device__ __forceinline__ uint32_t unit_offset(int rows, int r, int u) {
   return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
-}
-
-// two values of a key times f1 + f2: returns the high parts, and the low ones in `lo`
-__device__ __forceinline__ uint32_t split_key(uint32_t k, __nv_bfloat162 f1, __nv_bfloat162 f2, uint32_t& lo) {
-  const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&k);
-  const __nv_bfloat162 hi = __hmul2(x, f1);
-  const __nv_bfloat162 l = __hfma2(x, f2, __hfma2(x, f1, __hneg2(hi)));
-  lo = *reinterpret_cast<const uint32_t*>(&l);
-  return *reinterpret_cast<const uint32_t*>(&hi);
-}
-
-__device__ __forceinline__ void store_32b(void* to, const uint32_t* z) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(z[0]), "r"(z[1]), "r"(z[2]),
-               "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
-               : "memory");
 }
 
 // Column and row of a lane: with d1 = 64 lanes 64-127 hold a second copy of the
@@ -159,45 +146,56 @@ __device__ __forceinline__ void write_state(uint32_t lane_base, const StateLane<
   }
 }
 
-// Key row j of a chunk of n tokens, scaled: hi in place in tB, lo returned.  The
-// factor is taken as f1 + f2 (error 2^-18): with hi = f1 k rounded, f1 k - hi is
-// a bf16 value, and lo is that and f2 k, rounded.  Rows past the end (another
-// sequence's, or nothing) are cleared, in tC too.
-template <int D1, int D2>
-__device__ __forceinline__ void scale_key_row(uint8_t* tB, uint8_t* tC, int j, int n, float fac,
-                                              uint32_t (&lo)[D1 / 2]) {
-  const __nv_bfloat16 f1 = __float2bfloat16_rn(fac), f2 = __float2bfloat16_rn(fac - __bfloat162float(f1));
-  const __nv_bfloat162 g1 = __halves2bfloat162(f1, f1), g2 = __halves2bfloat162(f2, f2);
-  if (j < n) {
+// Key row j of a chunk of n tokens, scaled, as hi + lo.  The factor is taken as
+// f1 + f2 (error 2^-18): with hi = f1 k rounded, f1 k - hi is a bf16 value, and
+// lo is that and f2 k, rounded.  Rows past the end (another sequence's, or
+// nothing) count as zeros, and are cleared in the C tile.
+struct KeyFactor {
+  __nv_bfloat162 f1, f2;
+  __device__ __forceinline__ explicit KeyFactor(float f) {
+    const __nv_bfloat16 a = __float2bfloat16_rn(f), b = __float2bfloat16_rn(f - __bfloat162float(a));
+    f1 = __halves2bfloat162(a, a);
+    f2 = __halves2bfloat162(b, b);
+  }
+  __device__ __forceinline__ uint32_t split(uint32_t k, uint32_t& lo) const {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&k);
+    const __nv_bfloat162 hi = __hmul2(x, f1), l = __hfma2(x, f2, __hfma2(x, f1, __hneg2(hi)));
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+    return *reinterpret_cast<const uint32_t*>(&hi);
+  }
+};
+
+// One half of a row of D values: its high parts in place, its low parts to registers
+template <int D>
+__device__ __forceinline__ void split_half(uint8_t* tB, int j, int half, bool live, const KeyFactor& f,
+                                           uint32_t (&lo)[D / 4]) {
 #pragma unroll
-    for (int u = 0; u < D1 / 8; ++u) {
-      uint4* at = reinterpret_cast<uint4*>(tB + unit_offset(kChunk, j, u));
-      const uint4 in = *at;
-      uint4 hi;
-      hi.x = split_key(in.x, g1, g2, lo[4 * u]);
-      hi.y = split_key(in.y, g1, g2, lo[4 * u + 1]);
-      hi.z = split_key(in.z, g1, g2, lo[4 * u + 2]);
-      hi.w = split_key(in.w, g1, g2, lo[4 * u + 3]);
-      *at = hi;
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < D1 / 8; ++u) {
-      *reinterpret_cast<uint4*>(tB + unit_offset(kChunk, j, u)) = make_uint4(0u, 0u, 0u, 0u);
-      lo[4 * u] = lo[4 * u + 1] = lo[4 * u + 2] = lo[4 * u + 3] = 0u;
-    }
-#pragma unroll
-    for (int u = 0; u < D2 / 8; ++u)
-      *reinterpret_cast<uint4*>(tC + unit_offset(kChunk, j, u)) = make_uint4(0u, 0u, 0u, 0u);
+  for (int u = 0; u < D / 16; ++u) {
+    uint4* at = reinterpret_cast<uint4*>(tB + unit_offset(kChunk, j, half * (D / 16) + u));
+    uint4 x = *at;
+    if (!live) x = make_uint4(0u, 0u, 0u, 0u);
+    uint4 hi;
+    hi.x = f.split(x.x, lo[4 * u]);
+    hi.y = f.split(x.y, lo[4 * u + 1]);
+    hi.z = f.split(x.z, lo[4 * u + 2]);
+    hi.w = f.split(x.w, lo[4 * u + 3]);
+    *at = hi;
   }
 }
-
-template <int D1>
-__device__ __forceinline__ void write_low_row(uint8_t* tA, int j, const uint32_t (&lo)[D1 / 2]) {
+// the low parts to the A tile
+template <int D>
+__device__ __forceinline__ void write_half(uint8_t* tA, int j, int half, const uint32_t (&lo)[D / 4]) {
 #pragma unroll
-  for (int u = 0; u < D1 / 8; ++u)
-    *reinterpret_cast<uint4*>(tA + unit_offset(kChunk, j, u)) =
+  for (int u = 0; u < D / 16; ++u)
+    *reinterpret_cast<uint4*>(tA + unit_offset(kChunk, j, half * (D / 16) + u)) =
         make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+}
+// a half row of zeros
+template <int D>
+__device__ __forceinline__ void clear_half(uint8_t* tile, int j, int half) {
+#pragma unroll
+  for (int u = 0; u < D / 16; ++u)
+    *reinterpret_cast<uint4*>(tile + unit_offset(kChunk, j, half * (D / 16) + u)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // descriptors of the state's products: scaled keys (M-major), and the C tile (N-major)
@@ -211,16 +209,19 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   using C = Cfg<D1, D2>;
   constexpr int kStages = C::kStages;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::offBar);
-  uint64_t* full = bars;               // [kStages] tiles landed
-  uint64_t* p_full = full + kStages;   // P in TMEM
-  uint64_t* w_full = p_full + 1;       // W written (128)
-  uint64_t* s_ready = w_full + 1;      // S scaled and copied (128)
-  uint64_t* a_done = s_ready + 1;      // A has met B and S: its tile takes lo
-  uint64_t* hi_full = a_done + 1;      // hi written, rows past the end cleared (128)
-  uint64_t* lo_full = hi_full + 1;     // lo written (128)
+  uint64_t* full = bars;               // [kStages] C landed, and B where out does not need its tile
+  uint64_t* late = full + kStages;     // [kStages] the other tiles landed
+  uint64_t* staged = late + kStages;   // [kStages] out in shared memory (256)
+  uint64_t* p_full = staged + kStages; // P in TMEM
+  uint64_t* w_full = p_full + 1;       // W written (256)
+  uint64_t* s_copied = w_full + 1;     // S copied to shared memory (128)
+  uint64_t* s_scaled = s_copied + 1;   // S scaled (128)
+  uint64_t* a_done = s_scaled + 1;     // A has met B and S: its tile takes lo
+  uint64_t* hi_full = a_done + 1;      // hi written, rows past the end cleared (256)
+  uint64_t* lo_full = hi_full + 1;     // lo written (256)
   uint64_t* o_full = lo_full + 1;      // both accumulators of out complete
-  uint64_t* o_free = o_full + 1;       // and read (128)
-  uint64_t* s_done = o_free + 1;       // S advanced; the chunk's tiles are free
+  uint64_t* o_free = o_full + 1;       // and read (256)
+  uint64_t* s_done = o_free + 1;       // S advanced
   uint64_t* mma_done = s_done + 1;     // every MMA issued has completed
   float* pw = reinterpret_cast<float*>(smem + C::offPow);
   float* col = reinterpret_cast<float*>(smem + C::offCol);
@@ -234,36 +235,53 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   // c-th chunk walked: its first token and its tokens
   auto chunk_t = [&](int c) { return f.t0 + (rev ? n_chunks - 1 - c : c) * kChunk; };
   auto chunk_n = [&](int c) { return min(kChunk, f.t1 - chunk_t(c)); };
-  // tiles of a chunk (one thread)
+  // tiles of a chunk (one thread): those that are free once its predecessor in
+  // the stage has been multiplied, and those that its out leaves through
+  auto load_b = [&](uint8_t* base, uint64_t* bar, int t) {
+#pragma unroll
+    for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + C::kA + x * 16384, &w.b, bar, 64 * x, h, t);
+  };
   auto load = [&](int c) {
     const int st = c % kStages, t = chunk_t(c);
     uint8_t* base = smem + C::offStage + st * C::kStage;
-    mbar_arrive_expect_tx(full + st, C::kStage);
-#pragma unroll
-    for (int x = 0; x < D1 / 64; ++x) {
-      tma_load_3d(base + x * 16384, &w.a, full + st, 64 * x, h, t);
-      tma_load_3d(base + C::kA + x * 16384, &w.b, full + st, 64 * x, h, t);
-    }
+    mbar_arrive_expect_tx(full + st, C::kC + (C::kLateB ? 0 : C::kA));
+    if (!C::kLateB) load_b(base, full + st, t);
 #pragma unroll
     for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + 2 * C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
   };
+  auto load_late = [&](int c) {
+    const int st = c % kStages, t = chunk_t(c);
+    uint8_t* base = smem + C::offStage + st * C::kStage;
+    mbar_arrive_expect_tx(late + st, C::kA + (C::kLateB ? C::kA : 0));
+#pragma unroll
+    for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + x * 16384, &w.a, late + st, 64 * x, h, t);
+    if (C::kLateB) load_b(base, late + st, t);
+  };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(late + s, 1);
+      mbar_init(staged + s, 256);
+    }
     mbar_init(p_full, 1);
-    mbar_init(w_full, 128);
-    mbar_init(s_ready, 128);
+    mbar_init(w_full, 256);
+    mbar_init(s_copied, 128);
+    mbar_init(s_scaled, 128);
     mbar_init(a_done, 1);
-    mbar_init(hi_full, 128);
-    mbar_init(lo_full, 128);
+    mbar_init(hi_full, 256);
+    mbar_init(lo_full, 256);
     mbar_init(o_full, 1);
-    mbar_init(o_free, 128);
+    mbar_init(o_free, 256);
     mbar_init(s_done, 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
-    for (int c = 0; c < min(kStages, n_chunks); ++c) load(c);
+    for (int c = 0; c < min(kStages, n_chunks); ++c) {
+      load_late(c);
+      load(c);
+    }
   }
   const float g = used_log_decay(p.log_decay[h], p.wc.status);
   if (threadIdx.x >= 64 && threadIdx.x < 64 + 129) pw[threadIdx.x - 64] = expf(g * (float)(threadIdx.x - 64));
@@ -281,7 +299,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   const WaitEnv env{p.wc.status, abort_flag, p.wc.limit};
 
   if (warp < 4) {
-    // --------------------------------------------------------------- S; warp 0: every copy and MMA
+    // --------------------------------------------------------------- S
     const int quarter = warp;
     const StateLane<D1, D2> l(quarter, lane);
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colS;
@@ -300,17 +318,18 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
                      ? w.fin + ((long long)f.row * p.H + h) * size
                      : nullptr;
     // a block of 32 columns of the state before a chunk: its copy, and itself scaled
-    auto put = [&](int b, const uint32_t (&r)[32], uint64_t keep) {
-      if (l.own(b)) {
+    auto put_copy = [&](int b, const uint32_t (&r)[32]) {
+      if (!l.own(b)) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t z[4];
+      for (int e = 0; e < 4; ++e) {
+        uint32_t z[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
-          *reinterpret_cast<uint4*>(copy + unit_offset(D1, l.row, 4 * b + e)) = make_uint4(z[0], z[1], z[2], z[3]);
-        }
+        for (int k = 0; k < 4; ++k)
+          z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
+        *reinterpret_cast<uint4*>(copy + unit_offset(D1, l.row, 4 * b + e)) = make_uint4(z[0], z[1], z[2], z[3]);
       }
+    };
+    auto put_scaled = [&](int b, const uint32_t (&r)[32], uint64_t keep) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         uint32_t z[16];
@@ -323,29 +342,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
         tmem_st16(lane_base + 32 * b + 16 * s, z);
       }
     };
-    constexpr uint32_t id_p = idesc_bf16(128, 128, false, false);  // A, B both K-major
-    constexpr uint32_t id_o = idesc_bf16(128, D2, false, true);    // A or W, and C or the copy of S (N-major)
-    constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);     // B^T (M-major), C (N-major)
-    const uint32_t sStage = smem_u32(smem + C::offStage);
-    const uint64_t dcopy = smem_desc(smem_u32(copy), D1 * 128, 1024, kSw128);
-    int loaded = min(kStages, n_chunks);
     if (split) griddep_wait();  // the scan's states
     for (int c = 0; c < n_chunks; ++c) {
-      const int st = c % kStages;
-      const uint32_t sA = sStage + st * C::kStage, sB = sA + C::kA, sC = sB + C::kA;
-      const uint64_t dA = smem_desc(sA, 16, 1024, kSw128), dC = smem_desc(sC, 16384, 1024, kSw128);
-      if (warp == 0) {
-        if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
-        tc_fence_after();
-        const uint64_t dB = smem_desc(sB, 16, 1024, kSw128);
-        // over W of the chunk before only after its product, which was issued before
-#pragma unroll
-        for (int ks = 0; ks < D1 / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-          mma_ss_w(tmem + C::colP, desc_add(dA, off), desc_add(dB, off), id_p, ks > 0);
-        }
-        mma_commit_w(p_full);
-      }
       const uint32_t kf = __float_as_uint(pw[chunk_n(c)]);
       const uint64_t keep = f32x2(kf, kf);
       if (c == 0) {
@@ -367,58 +365,36 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
             for (int e = 0; e < 32; ++e)
               r[e] = src ? __float_as_uint(src[(long long)(32 * b + e) * D1 + l.row]) : 0u;
           }
-          put(b, r, keep);
+          put_copy(b, r);
+          put_scaled(b, r, keep);
         }
+        fence_proxy_async_smem();
+        mbar_arrive(s_copied);
       } else {
         if (!mbar_wait_w(s_done, (c - 1) & 1, env)) break;
         tc_fence_after();
-        if (warp == 0 && loaded < n_chunks) {  // into the tiles of the chunk before
-          if (lane == 0) load(loaded);
-          ++loaded;
-          __syncwarp();
-        }
-        // two blocks of 32 columns in flight
+        // the copy first: A S waits for it, and the products onto S only later for the rest
 #pragma unroll 1
-        for (int b = 0; b < D2 / 32; b += 2) {
-          uint32_t r0[32], r1[32];
-          tmem_ld32(lane_base + 32 * b, r0);
-          tmem_ld32(lane_base + 32 * b + 32, r1);
+        for (int b = 0; b < D2 / 32; ++b) {
+          uint32_t r[32];
+          if (!l.own(b)) continue;
+          tmem_ld32(lane_base + 32 * b, r);
           tmem_wait_ld();
-          put(b, r0, keep);
-          put(b + 1, r1, keep);
+          put_copy(b, r);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(s_copied);
+#pragma unroll 1
+        for (int b = 0; b < D2 / 32; ++b) {
+          uint32_t r[32];
+          tmem_ld32(lane_base + 32 * b, r);
+          tmem_wait_ld();
+          put_scaled(b, r, keep);
         }
       }
       tmem_wait_st();
-      fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(s_ready);
-      if (warp != 0) continue;
-      if (!mbar_wait_w(s_ready, c & 1, env)) break;
-      if (c > 0 && !mbar_wait_w(o_free, (c - 1) & 1, env)) break;
-      tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < D1 / 16; ++ks)
-        mma_ss_w(tmem + C::colE, desc_add(dA, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dcopy, ks * 2048), id_o,
-                 ks > 0);
-      mma_commit_w(a_done);
-      if (!mbar_wait_w(hi_full, c & 1, env)) break;
-      tc_fence_after();
-      const uint64_t dHi = key_desc<D1>(sB), dLo = key_desc<D1>(sA);
-#pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks)
-        mma_ss_w(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
-      if (!mbar_wait_w(w_full, c & 1, env)) break;
-      tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks)  // keys 16 ks ..: W columns 8 ks ..
-        mma_ts_w(tmem + C::colI, tmem + C::colP + ks * 8, desc_add(dC, ks * 2048), id_o, ks > 0);
-      mma_commit_w(o_full);
-      if (!mbar_wait_w(lo_full, c & 1, env)) break;
-      tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks)
-        mma_ss_w(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
-      mma_commit_w(s_done);
+      mbar_arrive(s_scaled);
     }
     if (n_chunks > 0) {
       if (mbar_wait_w(s_done, (n_chunks - 1) & 1, env) && dst) {
@@ -431,33 +407,30 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
             src ? src[transposed ? (long long)j * D1 + l.row : (long long)l.row * D2 + j] : 0.f;
     }
     if (!split) griddep_wait();  // a grid ends after those it was launched behind
-    if (warp == 0) {
-      // every MMA and copy that was issued ends before the CTA does
-      mma_commit_w(mma_done);
-      mbar_wait_drain(mma_done, 0);
-      for (int c = max(loaded - kStages, 0); c < loaded; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
-    }
-  } else if (warp < 8) {
-    // --------------------------------------------------------------- W
-    const int quarter = warp % 4, i = quarter * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colP;
+  } else if (warp < 12) {
+    // --------------------------------------------------------------- W and out
+    const int quarter = warp % 4, half = warp >= 8 ? 1 : 0;
+    const int i = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     // Left of the diagonal, for the columns j0 .. j1 = j0 + 31 of a block,
     // a^(i-j) = a^(i-j1) a^(j1-j), both exponents >= 0; backwards a^(j-i) =
     // a^(j0-i) a^(j-j0) right of it: a factor of the row and one of the
-    // column, the same for all blocks.
+    // column, the same for all blocks.  Of the four blocks of a row, one warp
+    // takes the outer two and the other the inner two.
     for (int c = 0; c < n_chunks; ++c) {
       const int n = chunk_n(c);
       if (!mbar_wait_w(p_full, c & 1, env)) break;
       tc_fence_after();
-#pragma unroll
-      for (int bb = 0; bb < 4; ++bb) {
+#pragma unroll 1
+      for (int y = 0; y < 2; ++y) {
+        const int bb = half ? 1 + y : 3 * y;
         uint32_t x[16];
         if (rev ? bb < quarter : bb > quarter) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = 0u;
         } else {
           uint32_t r[32];
-          tmem_ld32(lane_base + 32 * bb, r);
+          tmem_ld32(lane_base + C::colP + 32 * bb, r);
           tmem_wait_ld();
           if (bb != quarter) {
             const uint32_t f = __float_as_uint(w.s_intra * pw[rev ? 32 * bb - i : i - 32 * bb - 31]);
@@ -476,9 +449,9 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float w0 = rev ? t[2 * e] : t[-2 * e], w1 = rev ? t[2 * e + 1] : t[-2 * e - 1];
-              const uint32_t y = pack_bf16x2(__uint_as_float(r[2 * e]) * w0, __uint_as_float(r[2 * e + 1]) * w1);
+              const uint32_t v = pack_bf16x2(__uint_as_float(r[2 * e]) * w0, __uint_as_float(r[2 * e + 1]) * w1);
               const bool k0 = rev ? 2 * e >= lane : 2 * e <= lane, k1 = rev ? 2 * e + 1 >= lane : 2 * e + 1 <= lane;
-              x[e] = y & ((k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u));
+              x[e] = v & ((k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u));
             }
           }
           if (rev && 32 * bb + 32 > n) {  // columns past the end hold another sequence's rows
@@ -489,68 +462,153 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
             }
           }
         }
-        tmem_st16(lane_base + 16 * bb, x);
+        tmem_st16(lane_base + C::colP + 32 * bb, x);
       }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(w_full);
-    }
-  } else if (warp < 12) {
-    // --------------------------------------------------------------- out = W C + s_inter a^reach A S
-    const int quarter = warp % 4, i = quarter * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    // stores of 32 bytes, where every row starts on such a boundary
-    const bool wide = ((reinterpret_cast<uintptr_t>(w.out) | (uintptr_t)(w.out_stride * 2)) & 31) == 0;
-    for (int c = 0; c < n_chunks; ++c) {
-      const int n = chunk_n(c);
+      // out = W C + s_inter a^reach A S
       const uint32_t f = __float_as_uint(w.s_inter * pw[rev ? max(n - 1 - i, 0) : i + 1]);
       const uint64_t reach = f32x2(f, f);
-      __nv_bfloat16* orow = w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2;
+      uint8_t* stage = smem + C::offStage + c % kStages * C::kStage;
       if (!mbar_wait_w(o_full, c & 1, env)) break;
       tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < D2 / 64; ++b) {
+        uint32_t z[16];
 #pragma unroll
-      for (int b = 0; b < D2 / 32; ++b) {
-        uint32_t x[32], y[32], z[16];
-        tmem_ld32(lane_base + C::colI + 32 * b, x);
-        tmem_ld32(lane_base + C::colE + 32 * b, y);
-        tmem_wait_ld();
-        if (b == D2 / 32 - 1) {
+        for (int s = 0; s < 2; ++s) {
+          uint32_t x[16], y[16];
+          tmem_ld16(lane_base + C::colI + half * (D2 / 2) + 32 * b + 16 * s, x);
+          tmem_ld16(lane_base + C::colE + half * (D2 / 2) + 32 * b + 16 * s, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint64_t v = f32x2_fma(reach, f32x2(y[2 * e], y[2 * e + 1]), f32x2(x[2 * e], x[2 * e + 1]));
+            z[8 * s + e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
+          }
+        }
+        if (b == D2 / 64 - 1) {
           tc_fence_before();
           mbar_arrive(o_free);
         }
+        if (n == kChunk) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint64_t v = f32x2_fma(reach, f32x2(y[2 * e], y[2 * e + 1]), f32x2(x[2 * e], x[2 * e + 1]));
-          z[e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
-        }
-        if (i < n) {
-          if (wide) {
-            store_32b(orow + 32 * b, z);
-            store_32b(orow + 32 * b + 16, z + 8);
-          } else {
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(stage + unit_offset(kChunk, i, half * (D2 / 16) + 4 * b + e)) =
+                make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+        } else if (i < n) {  // a copy of the whole tile would reach into the next sequence
+          __nv_bfloat16* orow =
+              w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + half * (D2 / 2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(orow + 32 * b + 8 * e) =
-                  make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(orow + 32 * b + 8 * e) =
+                make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
         }
       }
+      fence_proxy_async_smem();
+      mbar_arrive(staged + c % kStages);
     }
+  } else if (warp == 21) {
+    // --------------------------------------------------------------- out to memory, then the tiles it used
+    int loaded = min(kStages, n_chunks);
+    for (int c = 0; c < n_chunks; ++c) {
+      const int st = c % kStages;
+      if (!mbar_wait_w(staged + st, (c / kStages) & 1, env)) break;
+      if (lane == 0) {
+        if (chunk_n(c) == kChunk) {
+#pragma unroll
+          for (int x = 0; x < D2 / 64; ++x)
+            tma_store_3d(&w.o, smem + C::offStage + st * C::kStage + x * 16384, 64 * x, h, chunk_t(c));
+          bulk_commit_group();
+          bulk_wait_read_all();
+        }
+        if (loaded < n_chunks) load_late(loaded);
+      }
+      if (loaded < n_chunks) ++loaded;
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_all();
+    for (int c = max(loaded - kStages, 0); c < loaded; ++c) mbar_wait_drain(late + c % kStages, (c / kStages) & 1);
+  } else if (warp == 20) {
+    // --------------------------------------------------------------- every copy and MMA
+    constexpr uint32_t id_p = idesc_bf16(128, 128, false, false);  // A, B both K-major
+    constexpr uint32_t id_o = idesc_bf16(128, D2, false, true);    // A or W, and C or the copy of S (N-major)
+    constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);     // B^T (M-major), C (N-major)
+    const uint32_t sStage = smem_u32(smem + C::offStage);
+    const uint64_t dcopy = smem_desc(smem_u32(smem + C::offCopy), D1 * 128, 1024, kSw128);
+    int loaded = min(kStages, n_chunks);
+    for (int c = 0; c < n_chunks; ++c) {
+      const int st = c % kStages;
+      const uint32_t sA = sStage + st * C::kStage, sB = sA + C::kA, sC = sB + C::kA;
+      const uint64_t dA = smem_desc(sA, 16, 1024, kSw128), dC = smem_desc(sC, 16384, 1024, kSw128);
+      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
+      if (!mbar_wait_w(late + st, (c / kStages) & 1, env)) break;
+      tc_fence_after();
+      const uint64_t dB = smem_desc(sB, 16, 1024, kSw128);
+      // over W of the chunk before only after its product, which was issued before
+#pragma unroll
+      for (int ks = 0; ks < D1 / 16; ++ks) {
+        const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+        mma_ss_w(tmem + C::colP, desc_add(dA, off), desc_add(dB, off), id_p, ks > 0);
+      }
+      mma_commit_w(p_full);
+      if (c > 0 && loaded < n_chunks) {  // into the tiles of the chunk before
+        if (!mbar_wait_w(o_full, (c - 1) & 1, env)) break;
+        if (lane == 0) load(loaded);
+        ++loaded;
+        __syncwarp();
+      }
+      if (!mbar_wait_w(s_copied, c & 1, env)) break;
+      if (c > 0 && !mbar_wait_w(o_free, (c - 1) & 1, env)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < D1 / 16; ++ks)
+        mma_ss_w(tmem + C::colE, desc_add(dA, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dcopy, ks * 2048), id_o,
+                 ks > 0);
+      mma_commit_w(a_done);
+      if (!mbar_wait_w(s_scaled, c & 1, env)) break;
+      if (!mbar_wait_w(hi_full, c & 1, env)) break;
+      tc_fence_after();
+      const uint64_t dHi = key_desc<D1>(sB), dLo = key_desc<D1>(sA);
+#pragma unroll
+      for (int ks = 0; ks < kChunk / 16; ++ks)
+        mma_ss_w(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+      if (!mbar_wait_w(lo_full, c & 1, env)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < kChunk / 16; ++ks)
+        mma_ss_w(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+      mma_commit_w(s_done);
+      if (!mbar_wait_w(w_full, c & 1, env)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < kChunk / 16; ++ks)  // keys 16 ks ..: at the start of the 32 columns they came from
+        mma_ts_w(tmem + C::colI, tmem + C::colP + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dC, ks * 2048), id_o, ks > 0);
+      mma_commit_w(o_full);
+    }
+    // every MMA and copy that was issued ends before the CTA does
+    mma_commit_w(mma_done);
+    mbar_wait_drain(mma_done, 0);
+    for (int c = max(loaded - kStages, 0); c < loaded; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
   } else {
     // --------------------------------------------------------------- B
-    const int j = (warp - 12) * 32 + lane;  // token of the chunk
+    const int j = (warp & 3) * 32 + lane, half = warp >= 16 ? 1 : 0;  // token of the chunk, half of its row
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages, n = chunk_n(c);
+      const bool live = j < n;
       uint8_t* tA = smem + C::offStage + st * C::kStage;
-      const float fac = j < n ? w.s_key * (rev ? pw[j + 1] : pw[n - 1 - j]) : 0.f;
+      const KeyFactor kf(live ? w.s_key * (rev ? pw[j + 1] : pw[n - 1 - j]) : 0.f);
+      uint32_t lo[D1 / 4];
       if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
+      if (C::kLateB && !mbar_wait_w(late + st, (c / kStages) & 1, env)) break;
+      if (!live) clear_half<D2>(tA + 2 * C::kA, j, half);
       if (!mbar_wait_w(p_full, c & 1, env)) break;
-      uint32_t lo[D1 / 2];
-      scale_key_row<D1, D2>(tA + C::kA, tA + 2 * C::kA, j, n, fac, lo);
+      split_half<D1>(tA + C::kA, j, half, live, kf, lo);
       fence_proxy_async_smem();
       mbar_arrive(hi_full);
       if (!mbar_wait_w(a_done, c & 1, env)) break;
-      write_low_row<D1>(tA, j, lo);
+      write_half<D1>(tA, j, half, lo);
       fence_proxy_async_smem();
       mbar_arrive(lo_full);
     }
@@ -579,11 +637,14 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
 //   sum_t a^(tokens of the segment after t) B_t C_t^T   (backwards: a^(tokens before t, and t))
 // With each key scaled for the segment's end nothing is carried from chunk to
 // chunk, so no product waits for another: bound by the loads of B and C.
-// Warps: 0 MMA, 1 TMA, 4-15 scale the keys in three groups, a chunk each.
+// Warps: 0 MMA, 1 TMA, 4-15 scale the keys in two or three groups, a chunk each.
 template <int D1, int D2>
 __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t* smem, const Found& f) {
   using C = Cfg<D1, D2>;
   constexpr int kStages = C::kStages;
+  // a stage always falls to the same group, so that no wait is ever a phase ahead
+  constexpr int kGroups = kStages % 3 == 0 ? 3 : 2;
+  static_assert(kStages % kGroups == 0, "groups of the scaling warps");
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::offBar);  // [kStages] tiles landed
   uint64_t* empty = full + kStages;                                // [kStages] tiles read
   uint64_t* scaled = empty + kStages;                              // [kStages] hi and lo written (128)
@@ -648,17 +709,23 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
       for (int c = max(issued - kStages, 0); c < issued; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 4 + 4 * kGroups) {
     const int j = (warp & 3) * 32 + lane;  // token of the chunk
-    for (int c = (warp >> 2) - 1; c < n_chunks; c += 3) {
+    for (int c = (warp >> 2) - 1; c < n_chunks; c += kGroups) {
       const int st = c % kStages, t = f.t0 + c * kChunk, n = min(kChunk, f.t1 - t);
       uint8_t* tA = smem + C::offStage + st * C::kStage;
       const float fac =
           j < n ? w.s_key * expf(g * (float)(w.reverse ? t + j + 1 - f.t0 : f.t1 - 1 - t - j)) : 0.f;
       if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
       uint32_t lo[D1 / 2];
-      scale_key_row<D1, D2>(tA + C::kA, tA + 2 * C::kA, j, n, fac, lo);
-      write_low_row<D1>(tA, j, lo);
+      const KeyFactor kf(fac);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t lo[D1 / 4];
+        split_half<D1>(tA + C::kA, j, half, j < n, kf, lo);
+        write_half<D1>(tA, j, half, lo);
+        if (j >= n) clear_half<D2>(tA + 2 * C::kA, j, half);
+      }
       fence_proxy_async_smem();
       mbar_arrive(scaled + st);
     }
@@ -700,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_walk_kernel(const __grid_co
       prefetch_tmap(&w.a);
       prefetch_tmap(&w.b);
       prefetch_tmap(&w.c);
+      prefetch_tmap(&w.o);
     }
   }
   __syncthreads();
@@ -896,7 +964,8 @@ cudaError_t launch_decay_walks(const DecayWalk* walks, int n, const DecayShape& 
     const DecayWalk& x = walks[i];
     WalkParams& w = p.w[i];
     if (!make_tmap(&w.a, x.a, x.d1, sh.H, sh.T, x.a_stride) || !make_tmap(&w.b, x.b, x.d1, sh.H, sh.T, x.b_stride) ||
-        !make_tmap(&w.c, x.c, x.d2, sh.H, sh.T, x.c_stride))
+        !make_tmap(&w.c, x.c, x.d2, sh.H, sh.T, x.c_stride) ||
+        !make_tmap(&w.o, x.out, x.d2, sh.H, sh.T, x.out_stride))
       return cudaErrorInvalidValue;
     w.out = static_cast<__nv_bfloat16*>(x.out);
     w.out_stride = x.out_stride;
