@@ -58,7 +58,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 704;  // at most 128 registers: more warps would spill, to L2, as shared memory leaves no L1
+constexpr int kThreads = 704, kSumThreads = 512;
 constexpr int kMaxWalks = 3;
 constexpr uint32_t kTmemCols = 512;
 
@@ -96,9 +96,8 @@ struct Cfg {
   static constexpr int offStage = 0;
   static constexpr int offCopy = kStages * kStage;
   static constexpr int offPow = offCopy + kCopy;        // a^0 .. a^128
-  static constexpr int offCol = offPow + 132 * 4;       // column factors of a full 32-column block
-  static constexpr int offDiag = offCol + 32 * 4;       // s_intra a^|x| for x = -31 .. 31, from [1]
-  static constexpr int offBar = offDiag + 64 * 4;
+  static constexpr int offWeight = offPow + 132 * 4;    // s_intra times the weight of (i, j), at 128 + j - i
+  static constexpr int offBar = offWeight + 256 * 4;
   static constexpr int kBars = 3 * kStages + 11;
   static constexpr int offMisc = offBar + kBars * 8;
   static constexpr int kBytes = offMisc + 64 + 1024;    // + alignment slack
@@ -165,30 +164,26 @@ struct KeyFactor {
   }
 };
 
-// One half of a row of D values: its high parts in place, its low parts to registers
+// One half of a row of D values, from its tile
 template <int D>
-__device__ __forceinline__ void split_half(uint8_t* tB, int j, int half, bool live, const KeyFactor& f,
-                                           uint32_t (&lo)[D / 4]) {
+__device__ __forceinline__ void split_half(const uint8_t* tile, int j, int half, const KeyFactor& f,
+                                           uint32_t (&hi)[D / 4], uint32_t (&lo)[D / 4]) {
 #pragma unroll
   for (int u = 0; u < D / 16; ++u) {
-    uint4* at = reinterpret_cast<uint4*>(tB + unit_offset(kChunk, j, half * (D / 16) + u));
-    uint4 x = *at;
-    if (!live) x = make_uint4(0u, 0u, 0u, 0u);
-    uint4 hi;
-    hi.x = f.split(x.x, lo[4 * u]);
-    hi.y = f.split(x.y, lo[4 * u + 1]);
-    hi.z = f.split(x.z, lo[4 * u + 2]);
-    hi.w = f.split(x.w, lo[4 * u + 3]);
-    *at = hi;
+    const uint4 x = *reinterpret_cast<const uint4*>(tile + unit_offset(kChunk, j, half * (D / 16) + u));
+    hi[4 * u] = f.split(x.x, lo[4 * u]);
+    hi[4 * u + 1] = f.split(x.y, lo[4 * u + 1]);
+    hi[4 * u + 2] = f.split(x.z, lo[4 * u + 2]);
+    hi[4 * u + 3] = f.split(x.w, lo[4 * u + 3]);
   }
 }
-// the low parts to the A tile
+// and to a tile
 template <int D>
-__device__ __forceinline__ void write_half(uint8_t* tA, int j, int half, const uint32_t (&lo)[D / 4]) {
+__device__ __forceinline__ void write_half(uint8_t* tile, int j, int half, const uint32_t (&x)[D / 4]) {
 #pragma unroll
   for (int u = 0; u < D / 16; ++u)
-    *reinterpret_cast<uint4*>(tA + unit_offset(kChunk, j, half * (D / 16) + u)) =
-        make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+    *reinterpret_cast<uint4*>(tile + unit_offset(kChunk, j, half * (D / 16) + u)) =
+        make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
 }
 // a half row of zeros
 template <int D>
@@ -224,8 +219,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   uint64_t* s_done = o_free + 1;       // S advanced
   uint64_t* mma_done = s_done + 1;     // every MMA issued has completed
   float* pw = reinterpret_cast<float*>(smem + C::offPow);
-  float* col = reinterpret_cast<float*>(smem + C::offCol);
-  float* diag = reinterpret_cast<float*>(smem + C::offDiag);
+  float* weight = reinterpret_cast<float*>(smem + C::offWeight);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offMisc + 4);
 
@@ -285,12 +279,10 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   }
   const float g = used_log_decay(p.log_decay[h], p.wc.status);
   if (threadIdx.x >= 64 && threadIdx.x < 64 + 129) pw[threadIdx.x - 64] = expf(g * (float)(threadIdx.x - 64));
-  if (threadIdx.x >= 224 && threadIdx.x < 256) {
-    const int j = threadIdx.x - 224;
-    col[j] = expf(g * (float)(rev ? j : 31 - j));
+  if (threadIdx.x >= 256 && threadIdx.x < 512) {
+    const int y = (int)threadIdx.x - 256 - 128;  // j - i
+    weight[y + 128] = (rev ? y >= 0 : y <= 0) ? w.s_intra * expf(g * fabsf((float)y)) : 0.f;
   }
-  if (threadIdx.x >= 256 && threadIdx.x < 256 + 64)
-    diag[threadIdx.x - 256] = w.s_intra * expf(g * fabsf((float)((int)threadIdx.x - 256 - 32)));
   if (warp == 1) tmem_alloc(tmem_holder, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -317,80 +309,52 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     float* dst = w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1)
                      ? w.fin + ((long long)f.row * p.H + h) * size
                      : nullptr;
-    // a block of 32 columns of the state before a chunk: its copy, and itself scaled
-    auto put_copy = [&](int b, const uint32_t (&r)[32]) {
-      if (!l.own(b)) return;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t z[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
-        *reinterpret_cast<uint4*>(copy + unit_offset(D1, l.row, 4 * b + e)) = make_uint4(z[0], z[1], z[2], z[3]);
-      }
-    };
-    auto put_scaled = [&](int b, const uint32_t (&r)[32], uint64_t keep) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint32_t z[16];
+    if (split) griddep_wait();  // the scan's states
+    if (n_chunks > 0) {
+#pragma unroll 1
+      for (int b = 0; b < D2 / 8; ++b) {
+        uint32_t r[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint64_t v = f32x2_mul(f32x2(r[16 * s + 2 * e], r[16 * s + 2 * e + 1]), keep);
-          z[2 * e] = (uint32_t)v;
-          z[2 * e + 1] = (uint32_t)(v >> 32);
+          const int j = 8 * b + e;
+          r[e] = src ? __float_as_uint(src[transposed ? j * D1 + l.row : l.row * D2 + j]) : 0u;
         }
-        tmem_st16(lane_base + 32 * b + 16 * s, z);
+        tmem_st8(lane_base + 8 * b, r);
       }
-    };
-    if (split) griddep_wait();  // the scan's states
+      tmem_wait_st();
+    }
     for (int c = 0; c < n_chunks; ++c) {
-      const uint32_t kf = __float_as_uint(pw[chunk_n(c)]);
-      const uint64_t keep = f32x2(kf, kf);
-      if (c == 0) {
-#pragma unroll 1
-        for (int b = 0; b < D2 / 32; ++b) {
-          uint32_t r[32];
-          if (src && !transposed) {
-            const float4* s4 = reinterpret_cast<const float4*>(src + (long long)l.row * D2 + 32 * b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 x = s4[e];
-              r[4 * e] = __float_as_uint(x.x);
-              r[4 * e + 1] = __float_as_uint(x.y);
-              r[4 * e + 2] = __float_as_uint(x.z);
-              r[4 * e + 3] = __float_as_uint(x.w);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              r[e] = src ? __float_as_uint(src[(long long)(32 * b + e) * D1 + l.row]) : 0u;
-          }
-          put_copy(b, r);
-          put_scaled(b, r, keep);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(s_copied);
-      } else {
+      if (c > 0) {
         if (!mbar_wait_w(s_done, (c - 1) & 1, env)) break;
         tc_fence_after();
-        // the copy first: A S waits for it, and the products onto S only later for the rest
+      }
+      // The state before the chunk: first its copy, which A S waits for, then
+      // itself scaled, for which the products onto it wait.
 #pragma unroll 1
-        for (int b = 0; b < D2 / 32; ++b) {
-          uint32_t r[32];
-          if (!l.own(b)) continue;
-          tmem_ld32(lane_base + 32 * b, r);
-          tmem_wait_ld();
-          put_copy(b, r);
+      for (int b = l.own0 / 32; b < l.own1 / 32; ++b) {
+        uint32_t r[32];
+        tmem_ld32(lane_base + 32 * b, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t z[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
+          *reinterpret_cast<uint4*>(copy + unit_offset(D1, l.row, 4 * b + e)) = make_uint4(z[0], z[1], z[2], z[3]);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(s_copied);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(s_copied);
+      const float keep = pw[chunk_n(c)];
 #pragma unroll 1
-        for (int b = 0; b < D2 / 32; ++b) {
-          uint32_t r[32];
-          tmem_ld32(lane_base + 32 * b, r);
-          tmem_wait_ld();
-          put_scaled(b, r, keep);
-        }
+      for (int b = 0; b < D2 / 16; ++b) {
+        uint32_t r[16];
+        tmem_ld16(lane_base + 16 * b, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(keep * __uint_as_float(r[e]));
+        tmem_st16(lane_base + 16 * b, r);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -412,11 +376,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     const int quarter = warp % 4, half = warp >= 8 ? 1 : 0;
     const int i = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    // Left of the diagonal, for the columns j0 .. j1 = j0 + 31 of a block,
-    // a^(i-j) = a^(i-j1) a^(j1-j), both exponents >= 0; backwards a^(j-i) =
-    // a^(j0-i) a^(j-j0) right of it: a factor of the row and one of the
-    // column, the same for all blocks.  Of the four blocks of a row, one warp
-    // takes the outer two and the other the inner two.
+    // Of the four blocks of 32 columns of a row, one warp takes the outer two and
+    // the other the inner two.
     for (int c = 0; c < n_chunks; ++c) {
       const int n = chunk_n(c);
       if (!mbar_wait_w(p_full, c & 1, env)) break;
@@ -432,33 +393,18 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
           uint32_t r[32];
           tmem_ld32(lane_base + C::colP + 32 * bb, r);
           tmem_wait_ld();
-          if (bb != quarter) {
-            const uint32_t f = __float_as_uint(w.s_intra * pw[rev ? 32 * bb - i : i - 32 * bb - 31]);
-            const uint64_t rf = f32x2(f, f);
+          const float* t = weight + 128 + 32 * bb - i;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const ulonglong2 cf = reinterpret_cast<const ulonglong2*>(col)[e / 2];
-              const uint64_t lo = f32x2_mul(f32x2_mul(f32x2(r[2 * e], r[2 * e + 1]), rf), cf.x);
-              const uint64_t hi = f32x2_mul(f32x2_mul(f32x2(r[2 * e + 2], r[2 * e + 3]), rf), cf.y);
-              x[e] = pack_bf16x2(f32x2_lo(lo), f32x2_hi(lo));
-              x[e + 1] = pack_bf16x2(f32x2_lo(hi), f32x2_hi(hi));
-            }
-          } else {
-            // the table holds s_intra a^|i-j|; what stands beyond the diagonal is cut off below
-            const float* t = diag + (rev ? 32 - lane : 32 + lane);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float w0 = rev ? t[2 * e] : t[-2 * e], w1 = rev ? t[2 * e + 1] : t[-2 * e - 1];
-              const uint32_t v = pack_bf16x2(__uint_as_float(r[2 * e]) * w0, __uint_as_float(r[2 * e + 1]) * w1);
-              const bool k0 = rev ? 2 * e >= lane : 2 * e <= lane, k1 = rev ? 2 * e + 1 >= lane : 2 * e + 1 <= lane;
-              x[e] = v & ((k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u));
-            }
-          }
-          if (rev && 32 * bb + 32 > n) {  // columns past the end hold another sequence's rows
+          for (int e = 0; e < 16; ++e)
+            x[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * t[2 * e], __uint_as_float(r[2 * e + 1]) * t[2 * e + 1]);
+          // what a weight of 0 does not remove if it is NaN or infinite: beyond the
+          // diagonal, and backwards columns past the end, another sequence's rows
+          const int first = rev ? i : 0, end = rev ? n : i + 1;
+          if (bb == quarter || (rev && 32 * bb + 32 > n)) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int j = 32 * bb + 2 * e;
-              x[e] = j >= n ? 0u : j + 1 >= n ? x[e] & 0xffffu : x[e];
+              x[e] &= (j >= first && j < end ? 0xffffu : 0u) | (j + 1 >= first && j + 1 < end ? 0xffff0000u : 0u);
             }
           }
         }
@@ -474,46 +420,45 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
       if (!mbar_wait_w(o_full, c & 1, env)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int b = 0; b < D2 / 64; ++b) {
-        uint32_t z[16];
+      for (int b = 0; b < D2 / 32; ++b) {  // 16 columns at a time
+        const int at = half * (D2 / 2) + 16 * b;
+        uint32_t x[16], y[16], z[8];
+        tmem_ld16(lane_base + C::colI + at, x);
+        tmem_ld16(lane_base + C::colE + at, y);
+        tmem_wait_ld();
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          uint32_t x[16], y[16];
-          tmem_ld16(lane_base + C::colI + half * (D2 / 2) + 32 * b + 16 * s, x);
-          tmem_ld16(lane_base + C::colE + half * (D2 / 2) + 32 * b + 16 * s, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint64_t v = f32x2_fma(reach, f32x2(y[2 * e], y[2 * e + 1]), f32x2(x[2 * e], x[2 * e + 1]));
-            z[8 * s + e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
-          }
-        }
-        if (b == D2 / 64 - 1) {
-          tc_fence_before();
-          mbar_arrive(o_free);
+        for (int e = 0; e < 8; ++e) {
+          const uint64_t v = f32x2_fma(reach, f32x2(y[2 * e], y[2 * e + 1]), f32x2(x[2 * e], x[2 * e + 1]));
+          z[e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
         }
         if (n == kChunk) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(stage + unit_offset(kChunk, i, half * (D2 / 16) + 4 * b + e)) =
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<uint4*>(stage + unit_offset(kChunk, i, at / 8 + e)) =
                 make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
         } else if (i < n) {  // a copy of the whole tile would reach into the next sequence
-          __nv_bfloat16* orow =
-              w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + half * (D2 / 2);
+          uint4* orow =
+              reinterpret_cast<uint4*>(w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + at);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(orow + 32 * b + 8 * e) =
-                make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+          for (int e = 0; e < 2; ++e) orow[e] = make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
         }
       }
+      tc_fence_before();
+      mbar_arrive(o_free);
       fence_proxy_async_smem();
       mbar_arrive(staged + c % kStages);
     }
   } else if (warp == 21) {
-    // --------------------------------------------------------------- out to memory, then the tiles it used
-    int loaded = min(kStages, n_chunks);
+    // --------------------------------------------------------------- copies: tiles in, out
+    int loaded = min(kStages, n_chunks), loaded_late = loaded;
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
+      if (!mbar_wait_w(o_full, c & 1, env)) break;  // the chunk's products are complete
+      if (loaded < n_chunks) {
+        if (lane == 0) load(loaded);
+        ++loaded;
+        __syncwarp();
+      }
       if (!mbar_wait_w(staged + st, (c / kStages) & 1, env)) break;
       if (lane == 0) {
         if (chunk_n(c) == kChunk) {
@@ -523,21 +468,23 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
           bulk_commit_group();
           bulk_wait_read_all();
         }
-        if (loaded < n_chunks) load_late(loaded);
+        if (loaded_late < n_chunks) load_late(loaded_late);
       }
-      if (loaded < n_chunks) ++loaded;
+      if (loaded_late < n_chunks) ++loaded_late;
       __syncwarp();
     }
+    // every copy that was issued ends before the CTA does
     if (lane == 0) bulk_wait_all();
-    for (int c = max(loaded - kStages, 0); c < loaded; ++c) mbar_wait_drain(late + c % kStages, (c / kStages) & 1);
+    for (int c = max(loaded - kStages, 0); c < loaded; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
+    for (int c = max(loaded_late - kStages, 0); c < loaded_late; ++c)
+      mbar_wait_drain(late + c % kStages, (c / kStages) & 1);
   } else if (warp == 20) {
-    // --------------------------------------------------------------- every copy and MMA
+    // --------------------------------------------------------------- MMA
     constexpr uint32_t id_p = idesc_bf16(128, 128, false, false);  // A, B both K-major
     constexpr uint32_t id_o = idesc_bf16(128, D2, false, true);    // A or W, and C or the copy of S (N-major)
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);     // B^T (M-major), C (N-major)
     const uint32_t sStage = smem_u32(smem + C::offStage);
     const uint64_t dcopy = smem_desc(smem_u32(smem + C::offCopy), D1 * 128, 1024, kSw128);
-    int loaded = min(kStages, n_chunks);
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
       const uint32_t sA = sStage + st * C::kStage, sB = sA + C::kA, sC = sB + C::kA;
@@ -553,12 +500,6 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
         mma_ss_w(tmem + C::colP, desc_add(dA, off), desc_add(dB, off), id_p, ks > 0);
       }
       mma_commit_w(p_full);
-      if (c > 0 && loaded < n_chunks) {  // into the tiles of the chunk before
-        if (!mbar_wait_w(o_full, (c - 1) & 1, env)) break;
-        if (lane == 0) load(loaded);
-        ++loaded;
-        __syncwarp();
-      }
       if (!mbar_wait_w(s_copied, c & 1, env)) break;
       if (c > 0 && !mbar_wait_w(o_free, (c - 1) & 1, env)) break;
       tc_fence_after();
@@ -587,10 +528,9 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
         mma_ts_w(tmem + C::colI, tmem + C::colP + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dC, ks * 2048), id_o, ks > 0);
       mma_commit_w(o_full);
     }
-    // every MMA and copy that was issued ends before the CTA does
+    // every MMA that was issued ends before the CTA does
     mma_commit_w(mma_done);
     mbar_wait_drain(mma_done, 0);
-    for (int c = max(loaded - kStages, 0); c < loaded; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
   } else {
     // --------------------------------------------------------------- B
     const int j = (warp & 3) * 32 + lane, half = warp >= 16 ? 1 : 0;  // token of the chunk, half of its row
@@ -599,12 +539,16 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
       const bool live = j < n;
       uint8_t* tA = smem + C::offStage + st * C::kStage;
       const KeyFactor kf(live ? w.s_key * (rev ? pw[j + 1] : pw[n - 1 - j]) : 0.f);
-      uint32_t lo[D1 / 4];
+      uint32_t hi[D1 / 4], lo[D1 / 4];
       if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
       if (C::kLateB && !mbar_wait_w(late + st, (c / kStages) & 1, env)) break;
-      if (!live) clear_half<D2>(tA + 2 * C::kA, j, half);
+      if (!live) {  // of P only what W drops comes from these rows
+        clear_half<D1>(tA + C::kA, j, half);
+        clear_half<D2>(tA + 2 * C::kA, j, half);
+      }
+      split_half<D1>(tA + C::kA, j, half, kf, hi, lo);
       if (!mbar_wait_w(p_full, c & 1, env)) break;
-      split_half<D1>(tA + C::kA, j, half, live, kf, lo);
+      write_half<D1>(tA + C::kA, j, half, hi);
       fence_proxy_async_smem();
       mbar_arrive(hi_full);
       if (!mbar_wait_w(a_done, c & 1, env)) break;
@@ -721,10 +665,14 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
       const KeyFactor kf(fac);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        uint32_t lo[D1 / 4];
-        split_half<D1>(tA + C::kA, j, half, j < n, kf, lo);
+        uint32_t hi[D1 / 4], lo[D1 / 4];
+        if (j >= n) {
+          clear_half<D1>(tA + C::kA, j, half);
+          clear_half<D2>(tA + 2 * C::kA, j, half);
+        }
+        split_half<D1>(tA + C::kA, j, half, kf, hi, lo);
+        write_half<D1>(tA + C::kA, j, half, hi);
         write_half<D1>(tA, j, half, lo);
-        if (j >= n) clear_half<D2>(tA + 2 * C::kA, j, half);
       }
       fence_proxy_async_smem();
       mbar_arrive(scaled + st);
@@ -747,7 +695,7 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
 
 // DA, DB: the widths (d1, d2) of the walks; a `swapped` walk has them exchanged.
 template <int DA, int DB, bool kSum>
-__global__ void __launch_bounds__(kThreads, 1) decay_walk_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Found found;
@@ -940,7 +888,7 @@ cudaError_t launch(const Params& p, const Plan& pl, cudaStream_t st) {
   }
   e = cudaFuncSetAttribute(decay_walk_kernel<DA, DB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  decay_walk_kernel<DA, DB, true><<<grid, kThreads, bytes, st>>>(p);
+  decay_walk_kernel<DA, DB, true><<<grid, kSumThreads, bytes, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const dim3 scan(DA * DB / 4 / kScanThreads * (unsigned)std::min(p.N, p.T / pl.L) * p.H * p.n_walks);
   e = launch_pdl(decay_scan_kernel, scan, dim3(kScanThreads), 0, st, p, DA, DB);
