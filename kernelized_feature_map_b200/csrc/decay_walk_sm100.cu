@@ -88,17 +88,17 @@ template <int D1, int D2>
 struct Cfg {
   static constexpr int kA = kChunk * D1 * 2, kC = kChunk * D2 * 2;  // tile bytes
   static constexpr int kStage = 2 * kA + kC;                         // [A | B | C]
-  // out leaves through the chunk's A tile, and where that is too small its B tile as well
-  static constexpr bool kLateB = kC > kA;
   static constexpr int kCopy = D1 * D2 * 2;
   static constexpr int kFit = (226 * 1024 - kCopy) / kStage;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;                // 2 (128, 128) .. 4 (64, 64)
   static constexpr int offStage = 0;
   static constexpr int offCopy = kStages * kStage;
-  static constexpr int offPow = offCopy + kCopy;        // a^0 .. a^128
-  static constexpr int offWeight = offPow + 132 * 4;    // s_intra times the weight of (i, j), at 128 + j - i
-  static constexpr int offBar = offWeight + 256 * 4;
-  static constexpr int kBars = 3 * kStages + 11;
+  // the weights a^|y| of y = j - i, 0 on the side that is not kept, twice, the second
+  // time one entry on, so that the pair at any lane's j is aligned in one of them
+  static constexpr int kWeights = 178;  // 18 banks on: the two copies' reads share no bank
+  static constexpr int offWeight = offCopy + kCopy;
+  static constexpr int offBar = offWeight + 2 * kWeights * 4;
+  static constexpr int kBars = 4 * kStages + 11;
   static constexpr int offMisc = offBar + kBars * 8;
   static constexpr int kBytes = offMisc + 64 + 1024;    // + alignment slack
   static constexpr uint32_t colP = 0, colI = 128, colE = 128 + D2, colS = 128 + 2 * D2;
@@ -114,6 +114,46 @@ struct Found {
 // 16-byte unit u (8 values) of row r in a tile of 128-byte swizzled rows, `rows` to a 64-column atom
 __device__ __forceinline__ uint32_t unit_offset(int rows, int r, int u) {
   return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+}
+
+// Bounded wait as mbar_wait_w of sm100.cuh, in less code: a walk has more than
+// twenty of them, and written out in full they, with other loops unrolled, came
+// to 92 KB, more than an SM's instruction cache keeps.  The abort flag is the
+// CTA's; the limit and the status word are the call's.
+__shared__ int abort_flag;
+__device__ __forceinline__ bool wait_on(const WaitCtl& wc, uint64_t* bar, uint32_t parity) {
+  bool ok = mbar_test_wait(bar, parity);
+  if (!ok) {
+    const long long t0 = clock64();
+    do {
+      if (*(volatile int*)&abort_flag) break;
+      if (clock64() - t0 >= wc.limit) {
+        abort_flag = 1;
+        report_status(wc.status, kErrTimeout);
+        break;
+      }
+      ok = mbar_try_wait_sleep(bar, parity);
+    } while (!ok);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// Of 16 values in bf16 pairs, those up to the last-th (from the
+// first-th on); the others become 0 whatever they are.
+__device__ __forceinline__ void keep_up_to(uint32_t (&x)[8], int last) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] &= __funnelshift_rc(0xffffffffu, 0u, (uint32_t)max(0, 16 - 16 * (last - 2 * e)));
+}
+__device__ __forceinline__ void keep_from(uint32_t (&x)[8], int first) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] &= __funnelshift_lc(0u, 0xffffffffu, (uint32_t)max(0, 16 * (first - 2 * e)));
 }
 
 // Column and row of a lane: with d1 = 64 lanes 64-127 hold a second copy of the
@@ -204,10 +244,11 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   using C = Cfg<D1, D2>;
   constexpr int kStages = C::kStages;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::offBar);
-  uint64_t* full = bars;               // [kStages] C landed, and B where out does not need its tile
-  uint64_t* late = full + kStages;     // [kStages] the other tiles landed
+  uint64_t* full = bars;               // [kStages] A and B landed
+  uint64_t* late = full + kStages;     // [kStages] C landed
   uint64_t* staged = late + kStages;   // [kStages] out in shared memory (256)
-  uint64_t* p_full = staged + kStages; // P in TMEM
+  uint64_t* done = staged + kStages;   // [kStages] every product of the chunk complete
+  uint64_t* p_full = done + kStages;   // P in TMEM
   uint64_t* w_full = p_full + 1;       // W written (256)
   uint64_t* s_copied = w_full + 1;     // S copied to shared memory (128)
   uint64_t* s_scaled = s_copied + 1;   // S scaled (128)
@@ -218,10 +259,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   uint64_t* o_free = o_full + 1;       // and read (256)
   uint64_t* s_done = o_free + 1;       // S advanced
   uint64_t* mma_done = s_done + 1;     // every MMA issued has completed
-  float* pw = reinterpret_cast<float*>(smem + C::offPow);
   float* weight = reinterpret_cast<float*>(smem + C::offWeight);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::offMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offMisc + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool rev = w.reverse != 0;
@@ -229,27 +268,25 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   // c-th chunk walked: its first token and its tokens
   auto chunk_t = [&](int c) { return f.t0 + (rev ? n_chunks - 1 - c : c) * kChunk; };
   auto chunk_n = [&](int c) { return min(kChunk, f.t1 - chunk_t(c)); };
-  // tiles of a chunk (one thread): those that are free once its predecessor in
-  // the stage has been multiplied, and those that its out leaves through
-  auto load_b = [&](uint8_t* base, uint64_t* bar, int t) {
-#pragma unroll
-    for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + C::kA + x * 16384, &w.b, bar, 64 * x, h, t);
-  };
+  // tiles of a chunk (one thread): A and B as soon as the chunk before it in the
+  // stage has been multiplied, C once that chunk's out, which leaves through its
+  // C tile, has left
   auto load = [&](int c) {
     const int st = c % kStages, t = chunk_t(c);
     uint8_t* base = smem + C::offStage + st * C::kStage;
-    mbar_arrive_expect_tx(full + st, C::kC + (C::kLateB ? 0 : C::kA));
-    if (!C::kLateB) load_b(base, full + st, t);
+    mbar_arrive_expect_tx(full + st, 2 * C::kA);
 #pragma unroll
-    for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + 2 * C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
+    for (int x = 0; x < D1 / 64; ++x) {
+      tma_load_3d(base + x * 16384, &w.a, full + st, 64 * x, h, t);
+      tma_load_3d(base + C::kA + x * 16384, &w.b, full + st, 64 * x, h, t);
+    }
   };
   auto load_late = [&](int c) {
     const int st = c % kStages, t = chunk_t(c);
     uint8_t* base = smem + C::offStage + st * C::kStage;
-    mbar_arrive_expect_tx(late + st, C::kA + (C::kLateB ? C::kA : 0));
+    mbar_arrive_expect_tx(late + st, C::kC);
 #pragma unroll
-    for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + x * 16384, &w.a, late + st, 64 * x, h, t);
-    if (C::kLateB) load_b(base, late + st, t);
+    for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + 2 * C::kA + x * 16384, &w.c, late + st, 64 * x, h, t);
   };
 
   if (threadIdx.x == 0) {
@@ -257,6 +294,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
       mbar_init(full + s, 1);
       mbar_init(late + s, 1);
       mbar_init(staged + s, 256);
+      mbar_init(done + s, 1);
     }
     mbar_init(p_full, 1);
     mbar_init(w_full, 256);
@@ -269,26 +307,28 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     mbar_init(o_free, 256);
     mbar_init(s_done, 1);
     mbar_init(mma_done, 1);
-    *abort_flag = 0;
+    abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
+#pragma unroll 1
     for (int c = 0; c < min(kStages, n_chunks); ++c) {
-      load_late(c);
       load(c);
+      load_late(c);
     }
   }
   const float g = used_log_decay(p.log_decay[h], p.wc.status);
-  if (threadIdx.x >= 64 && threadIdx.x < 64 + 129) pw[threadIdx.x - 64] = expf(g * (float)(threadIdx.x - 64));
-  if (threadIdx.x >= 256 && threadIdx.x < 512) {
-    const int y = (int)threadIdx.x - 256 - 128;  // j - i
-    weight[y + 128] = (rev ? y >= 0 : y <= 0) ? w.s_intra * expf(g * fabsf((float)y)) : 0.f;
+  const int y0 = rev ? -32 : -128;  // y of the first weight
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + 2 * C::kWeights) {
+    const int x = (int)threadIdx.x - 64, y = y0 + x % C::kWeights + x / C::kWeights;
+    weight[x] = (rev ? y >= 0 : y <= 0) ? expf(g * fabsf((float)y)) : 0.f;
   }
+  auto power = [&](int x) { return weight[rev ? 32 + x : 128 - x]; };  // a^x, x = 0 .. 128
   if (warp == 1) tmem_alloc(tmem_holder, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const WaitEnv env{p.wc.status, abort_flag, p.wc.limit};
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, bar, parity); };
 
   if (warp < 4) {
     // --------------------------------------------------------------- S
@@ -323,45 +363,64 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
       }
       tmem_wait_st();
     }
+#pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       if (c > 0) {
-        if (!mbar_wait_w(s_done, (c - 1) & 1, env)) break;
+        if (!wait(s_done, (c - 1) & 1)) break;
         tc_fence_after();
       }
       // The state before the chunk: first its copy, which A S waits for, then
       // itself scaled, for which the products onto it wait.
-#pragma unroll 1
-      for (int b = l.own0 / 32; b < l.own1 / 32; ++b) {
-        uint32_t r[32];
-        tmem_ld32(lane_base + 32 * b, r);
-        tmem_wait_ld();
+      uint32_t r[2][16];  // 16 columns, and the next 16 on their way
+      auto put_copy = [&](int at, const uint32_t (&x)[16]) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           uint32_t z[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
-          *reinterpret_cast<uint4*>(copy + unit_offset(D1, l.row, 4 * b + e)) = make_uint4(z[0], z[1], z[2], z[3]);
+            z[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]), __uint_as_float(x[8 * e + 2 * k + 1]));
+          *reinterpret_cast<uint4*>(copy + unit_offset(D1, l.row, at / 8 + e)) = make_uint4(z[0], z[1], z[2], z[3]);
         }
+      };
+      tmem_ld16(lane_base + l.own0, r[0]);
+#pragma unroll 1
+      for (int at = l.own0; at < l.own1; at += 32) {
+        tmem_wait_ld();
+        tmem_ld16(lane_base + at + 16, r[1]);
+        put_copy(at, r[0]);
+        tmem_wait_ld();
+        if (at + 32 < l.own1) tmem_ld16(lane_base + at + 32, r[0]);
+        put_copy(at + 16, r[1]);
       }
       fence_proxy_async_smem();
       mbar_arrive(s_copied);
-      const float keep = pw[chunk_n(c)];
-#pragma unroll 1
-      for (int b = 0; b < D2 / 16; ++b) {
-        uint32_t r[16];
-        tmem_ld16(lane_base + 16 * b, r);
-        tmem_wait_ld();
+      const uint32_t f0 = __float_as_uint(power(chunk_n(c)));
+      const uint64_t keep = f32x2(f0, f0);
+      auto put_scaled = [&](int at, uint32_t (&x)[16]) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(keep * __uint_as_float(r[e]));
-        tmem_st16(lane_base + 16 * b, r);
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t v = f32x2_mul(f32x2(x[2 * k], x[2 * k + 1]), keep);
+          x[2 * k] = (uint32_t)v;
+          x[2 * k + 1] = (uint32_t)(v >> 32);
+        }
+        tmem_st16(lane_base + at, x);
+      };
+      tmem_ld16(lane_base, r[0]);
+#pragma unroll 1
+      for (int at = 0; at < D2; at += 32) {
+        tmem_wait_ld();
+        tmem_ld16(lane_base + at + 16, r[1]);
+        put_scaled(at, r[0]);
+        tmem_wait_ld();
+        if (at + 32 < D2) tmem_ld16(lane_base + at + 32, r[0]);
+        put_scaled(at + 16, r[1]);
       }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(s_scaled);
     }
     if (n_chunks > 0) {
-      if (mbar_wait_w(s_done, (n_chunks - 1) & 1, env) && dst) {
+      if (wait(s_done, (n_chunks - 1) & 1) && dst) {
         tc_fence_after();
         write_state(lane_base, l, dst);
       }
@@ -378,93 +437,109 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     // Of the four blocks of 32 columns of a row, one warp takes the outer two and
     // the other the inner two.
+#pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int n = chunk_n(c);
-      if (!mbar_wait_w(p_full, c & 1, env)) break;
+      if (!wait(p_full, c & 1)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int y = 0; y < 2; ++y) {
-        const int bb = half ? 1 + y : 3 * y;
-        uint32_t x[16];
+      for (int y = 0; y < 4; ++y) {
+        const int bb = half ? 1 + (y >> 1) : 3 * (y >> 1), j0 = 32 * bb + 16 * (y & 1);  // columns j0 .. j0 + 15
+        uint32_t x[8];
         if (rev ? bb < quarter : bb > quarter) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = 0u;
+          for (int e = 0; e < 8; ++e) x[e] = 0u;
         } else {
-          uint32_t r[32];
-          tmem_ld32(lane_base + C::colP + 32 * bb, r);
+          uint32_t r[16];
+          tmem_ld16(lane_base + C::colP + j0, r);
           tmem_wait_ld();
-          const float* t = weight + 128 + 32 * bb - i;
+          const int at = j0 - i - y0;
+          const uint64_t* t = reinterpret_cast<const uint64_t*>(weight + (at & 1 ? C::kWeights + at - 1 : at));
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            x[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * t[2 * e], __uint_as_float(r[2 * e + 1]) * t[2 * e + 1]);
+          for (int e = 0; e < 8; ++e) {
+            const uint64_t v = f32x2_mul(f32x2(r[2 * e], r[2 * e + 1]), t[e]);
+            x[e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
+          }
           // what a weight of 0 does not remove if it is NaN or infinite: beyond the
           // diagonal, and backwards columns past the end, another sequence's rows
-          const int first = rev ? i : 0, end = rev ? n : i + 1;
-          if (bb == quarter || (rev && 32 * bb + 32 > n)) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int j = 32 * bb + 2 * e;
-              x[e] &= (j >= first && j < end ? 0xffffu : 0u) | (j + 1 >= first && j + 1 < end ? 0xffff0000u : 0u);
-            }
+          if (bb == quarter) {
+            if (rev)
+              keep_from(x, i - j0);
+            else
+              keep_up_to(x, i - j0);
           }
+          if (rev && j0 + 16 > n) keep_up_to(x, n - 1 - j0);
         }
-        tmem_st16(lane_base + C::colP + 32 * bb, x);
+        tmem_st8(lane_base + C::colP + 32 * bb + 8 * (y & 1), x);
       }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(w_full);
-      // out = W C + s_inter a^reach A S
-      const uint32_t f = __float_as_uint(w.s_inter * pw[rev ? max(n - 1 - i, 0) : i + 1]);
-      const uint64_t reach = f32x2(f, f);
-      uint8_t* stage = smem + C::offStage + c % kStages * C::kStage;
-      if (!mbar_wait_w(o_full, c & 1, env)) break;
+      // out = s_intra W C + s_inter a^reach A S
+      const uint32_t f0 = __float_as_uint(w.s_intra), f1 = __float_as_uint(w.s_inter * power(rev ? max(n - 1 - i, 0) : i + 1));
+      const uint64_t intra = f32x2(f0, f0), reach = f32x2(f1, f1);
+      if (!wait(o_full, c & 1)) break;
       tc_fence_after();
+      bool ok = true;
 #pragma unroll 1
-      for (int b = 0; b < D2 / 32; ++b) {  // 16 columns at a time
-        const int at = half * (D2 / 2) + 16 * b;
-        uint32_t x[16], y[16], z[8];
-        tmem_ld16(lane_base + C::colI + at, x);
-        tmem_ld16(lane_base + C::colE + at, y);
-        tmem_wait_ld();
+      for (int at = half * (D2 / 2); at < (half + 1) * (D2 / 2); at += 32) {
+        uint32_t z[16], x[2][8], y[2][8];
+        tmem_ld8(lane_base + C::colI + at, x[0]);
+        tmem_ld8(lane_base + C::colE + at, y[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint64_t v = f32x2_fma(reach, f32x2(y[2 * e], y[2 * e + 1]), f32x2(x[2 * e], x[2 * e + 1]));
-          z[e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
+        for (int b = 0; b < 4; ++b) {  // 8 columns, and the next 8 on their way
+          tmem_wait_ld();
+          if (b + 1 < 4) {
+            tmem_ld8(lane_base + C::colI + at + 8 * (b + 1), x[(b + 1) & 1]);
+            tmem_ld8(lane_base + C::colE + at + 8 * (b + 1), y[(b + 1) & 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t v = f32x2_fma(reach, f32x2(y[b & 1][2 * e], y[b & 1][2 * e + 1]),
+                                         f32x2_mul(intra, f32x2(x[b & 1][2 * e], x[b & 1][2 * e + 1])));
+            z[4 * b + e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
+          }
         }
-        if (n == kChunk) {
+        if (at + 32 == (half + 1) * (D2 / 2)) {
+          tc_fence_before();
+          mbar_arrive(o_free);
+        }
+        // through the C tile, once the last product has read it; a copy of a tile
+        // that is not full would reach into the next sequence
+        if (n == kChunk && at == half * (D2 / 2)) ok = wait(s_done, c & 1);
+        uint8_t* stage = smem + C::offStage + c % kStages * C::kStage + 2 * C::kA;
+        uint4* orow = reinterpret_cast<uint4*>(w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + at);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<uint4*>(stage + unit_offset(kChunk, i, at / 8 + e)) =
-                make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
-        } else if (i < n) {  // a copy of the whole tile would reach into the next sequence
-          uint4* orow =
-              reinterpret_cast<uint4*>(w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + at);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) orow[e] = make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+        for (int e = 0; e < 4; ++e) {
+          const uint4 v = make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+          if (n == kChunk)
+            *reinterpret_cast<uint4*>(stage + unit_offset(kChunk, i, at / 8 + e)) = v;
+          else if (i < n)
+            orow[e] = v;
         }
       }
-      tc_fence_before();
-      mbar_arrive(o_free);
+      if (!ok) break;
       fence_proxy_async_smem();
       mbar_arrive(staged + c % kStages);
     }
   } else if (warp == 21) {
     // --------------------------------------------------------------- copies: tiles in, out
     int loaded = min(kStages, n_chunks), loaded_late = loaded;
+#pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
-      if (!mbar_wait_w(o_full, c & 1, env)) break;  // the chunk's products are complete
+      if (!wait(done + st, (c / kStages) & 1)) break;
       if (loaded < n_chunks) {
         if (lane == 0) load(loaded);
         ++loaded;
         __syncwarp();
       }
-      if (!mbar_wait_w(staged + st, (c / kStages) & 1, env)) break;
+      if (!wait(staged + st, (c / kStages) & 1)) break;
       if (lane == 0) {
         if (chunk_n(c) == kChunk) {
 #pragma unroll
           for (int x = 0; x < D2 / 64; ++x)
-            tma_store_3d(&w.o, smem + C::offStage + st * C::kStage + x * 16384, 64 * x, h, chunk_t(c));
+            tma_store_3d(&w.o, smem + C::offStage + st * C::kStage + 2 * C::kA + x * 16384, 64 * x, h, chunk_t(c));
           bulk_commit_group();
           bulk_wait_read_all();
         }
@@ -475,7 +550,9 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     }
     // every copy that was issued ends before the CTA does
     if (lane == 0) bulk_wait_all();
+#pragma unroll 1
     for (int c = max(loaded - kStages, 0); c < loaded; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
+#pragma unroll 1
     for (int c = max(loaded_late - kStages, 0); c < loaded_late; ++c)
       mbar_wait_drain(late + c % kStages, (c / kStages) & 1);
   } else if (warp == 20) {
@@ -485,48 +562,60 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);     // B^T (M-major), C (N-major)
     const uint32_t sStage = smem_u32(smem + C::offStage);
     const uint64_t dcopy = smem_desc(smem_u32(smem + C::offCopy), D1 * 128, 1024, kSw128);
+#pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
       const uint32_t sA = sStage + st * C::kStage, sB = sA + C::kA, sC = sB + C::kA;
       const uint64_t dA = smem_desc(sA, 16, 1024, kSw128), dC = smem_desc(sC, 16384, 1024, kSw128);
-      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
-      if (!mbar_wait_w(late + st, (c / kStages) & 1, env)) break;
+      if (!wait(full + st, (c / kStages) & 1)) break;
       tc_fence_after();
       const uint64_t dB = smem_desc(sB, 16, 1024, kSw128);
       // over W of the chunk before only after its product, which was issued before
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < D1 / 16; ++ks) {
-        const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-        mma_ss_w(tmem + C::colP, desc_add(dA, off), desc_add(dB, off), id_p, ks > 0);
+        for (int ks = 0; ks < D1 / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+          mma_ss(tmem + C::colP, desc_add(dA, off), desc_add(dB, off), id_p, ks > 0);
+        }
+        mma_commit(p_full);
       }
-      mma_commit_w(p_full);
-      if (!mbar_wait_w(s_copied, c & 1, env)) break;
-      if (c > 0 && !mbar_wait_w(o_free, (c - 1) & 1, env)) break;
+      if (!wait(s_copied, c & 1)) break;
+      if (c > 0 && !wait(o_free, (c - 1) & 1)) break;
       tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < D1 / 16; ++ks)
-        mma_ss_w(tmem + C::colE, desc_add(dA, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dcopy, ks * 2048), id_o,
-                 ks > 0);
-      mma_commit_w(a_done);
-      if (!mbar_wait_w(s_scaled, c & 1, env)) break;
-      if (!mbar_wait_w(hi_full, c & 1, env)) break;
+        for (int ks = 0; ks < D1 / 16; ++ks)
+          mma_ss(tmem + C::colE, desc_add(dA, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dcopy, ks * 2048), id_o,
+                   ks > 0);
+        mma_commit(a_done);
+      }
+      if (!wait(s_scaled, c & 1)) break;
+      if (!wait(hi_full, c & 1)) break;
+      if (!wait(late + st, (c / kStages) & 1)) break;
       tc_fence_after();
       const uint64_t dHi = key_desc<D1>(sB), dLo = key_desc<D1>(sA);
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks)
-        mma_ss_w(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
-      if (!mbar_wait_w(lo_full, c & 1, env)) break;
+        for (int ks = 0; ks < kChunk / 16; ++ks)
+          mma_ss(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+      }
+      if (!wait(w_full, c & 1)) break;
       tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks)
-        mma_ss_w(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
-      mma_commit_w(s_done);
-      if (!mbar_wait_w(w_full, c & 1, env)) break;
+        for (int ks = 0; ks < kChunk / 16; ++ks)  // keys 16 ks ..: at the start of the 32 columns they came from
+          mma_ts(tmem + C::colI, tmem + C::colP + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dC, ks * 2048), id_o, ks > 0);
+        mma_commit(o_full);
+      }
+      if (!wait(lo_full, c & 1)) break;
       tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks)  // keys 16 ks ..: at the start of the 32 columns they came from
-        mma_ts_w(tmem + C::colI, tmem + C::colP + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dC, ks * 2048), id_o, ks > 0);
-      mma_commit_w(o_full);
+        for (int ks = 0; ks < kChunk / 16; ++ks)
+          mma_ss(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+        mma_commit(s_done);
+        mma_commit(done + st);
+      }
     }
     // every MMA that was issued ends before the CTA does
     mma_commit_w(mma_done);
@@ -534,24 +623,25 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
   } else {
     // --------------------------------------------------------------- B
     const int j = (warp & 3) * 32 + lane, half = warp >= 16 ? 1 : 0;  // token of the chunk, half of its row
+#pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages, n = chunk_n(c);
       const bool live = j < n;
       uint8_t* tA = smem + C::offStage + st * C::kStage;
-      const KeyFactor kf(live ? w.s_key * (rev ? pw[j + 1] : pw[n - 1 - j]) : 0.f);
+      const KeyFactor kf(live ? w.s_key * power(rev ? j + 1 : n - 1 - j) : 0.f);
       uint32_t hi[D1 / 4], lo[D1 / 4];
-      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
-      if (C::kLateB && !mbar_wait_w(late + st, (c / kStages) & 1, env)) break;
+      if (!wait(full + st, (c / kStages) & 1)) break;
+      if (n < kChunk && !wait(late + st, (c / kStages) & 1)) break;
       if (!live) {  // of P only what W drops comes from these rows
         clear_half<D1>(tA + C::kA, j, half);
         clear_half<D2>(tA + 2 * C::kA, j, half);
       }
       split_half<D1>(tA + C::kA, j, half, kf, hi, lo);
-      if (!mbar_wait_w(p_full, c & 1, env)) break;
+      if (!wait(p_full, c & 1)) break;
       write_half<D1>(tA + C::kA, j, half, hi);
       fence_proxy_async_smem();
       mbar_arrive(hi_full);
-      if (!mbar_wait_w(a_done, c & 1, env)) break;
+      if (!wait(a_done, c & 1)) break;
       write_half<D1>(tA, j, half, lo);
       fence_proxy_async_smem();
       mbar_arrive(lo_full);
@@ -594,7 +684,6 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
   uint64_t* scaled = empty + kStages;                              // [kStages] hi and lo written (128)
   uint64_t* mma_done = scaled + kStages;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::offMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
   if (threadIdx.x == 0) {
@@ -604,7 +693,7 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
       mbar_init(scaled + s, 128);
     }
     mbar_init(mma_done, 1);
-    *abort_flag = 0;
+    abort_flag = 0;
     fence_barrier_init();
   }
   const float g = used_log_decay(p.log_decay[h], p.wc.status);
@@ -613,17 +702,18 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const WaitEnv env{p.wc.status, abort_flag, p.wc.limit};
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, bar, parity); };
   if (warp == 0) {
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);
     const uint32_t sStage = smem_u32(smem + C::offStage);
+#pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
       const uint32_t sA = sStage + st * C::kStage;
       const uint64_t dLo = key_desc<D1>(sA), dHi = key_desc<D1>(sA + C::kA);
       const uint64_t dC = smem_desc(sA + 2 * C::kA, 16384, 1024, kSw128);
-      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
-      if (!mbar_wait_w(scaled + st, (c / kStages) & 1, env)) break;
+      if (!wait(full + st, (c / kStages) & 1)) break;
+      if (!wait(scaled + st, (c / kStages) & 1)) break;
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < kChunk / 16; ++ks)
@@ -636,31 +726,34 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
     mma_commit_w(mma_done);
     mbar_wait_drain(mma_done, 0);
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       int issued = 0;
-      for (int c = 0; c < n_chunks; ++c) {
+#pragma unroll 1
+      for (int c = 0; c < n_chunks; ++c, ++issued) {
         const int st = c % kStages, t = f.t0 + c * kChunk;
-        if (!mbar_wait(empty + st, ((c / kStages) & 1) ^ 1, env)) break;
+        if (!wait(empty + st, ((c / kStages) & 1) ^ 1)) break;
+        if (lane != 0) continue;
         uint8_t* base = smem + C::offStage + st * C::kStage + C::kA;
         mbar_arrive_expect_tx(full + st, C::kA + C::kC);
 #pragma unroll
         for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + x * 16384, &w.b, full + st, 64 * x, h, t);
 #pragma unroll
         for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
-        ++issued;
       }
       // every copy that was issued ends before the CTA does
+#pragma unroll 1
       for (int c = max(issued - kStages, 0); c < issued; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 4 + 4 * kGroups) {
     const int j = (warp & 3) * 32 + lane;  // token of the chunk
+#pragma unroll 1
     for (int c = (warp >> 2) - 1; c < n_chunks; c += kGroups) {
       const int st = c % kStages, t = f.t0 + c * kChunk, n = min(kChunk, f.t1 - t);
       uint8_t* tA = smem + C::offStage + st * C::kStage;
       const float fac =
           j < n ? w.s_key * expf(g * (float)(w.reverse ? t + j + 1 - f.t0 : f.t1 - 1 - t - j)) : 0.f;
-      if (!mbar_wait_w(full + st, (c / kStages) & 1, env)) break;
+      if (!wait(full + st, (c / kStages) & 1)) break;
       uint32_t lo[D1 / 2];
       const KeyFactor kf(fac);
 #pragma unroll 1
@@ -679,7 +772,7 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
     }
   }
   if (warp < 4) {
-    if (mbar_wait_w(mma_done, 0, env)) {
+    if (wait(mma_done, 0)) {
       tc_fence_after();
       write_state(tmem + ((uint32_t)(warp * 32) << 16) + C::colS, StateLane<D1, D2>(warp, lane),
                   w.rec + ((long long)(f.rec + f.seg) * p.H + h) * (D1 * D2));
