@@ -20,9 +20,9 @@ kata_status_t check_shape(int T, int H, int d, int dv, int N, kata_dtype_t dt) {
   if (dt != KATA_BF16 && dt != KATA_F32) return KATA_ERR_INVALID_ARG;
   if (!width_ok(d) || !width_ok(dv)) return KATA_ERR_UNSUPPORTED;
   if (T > kMaxTokens || N > kMaxSequences || H > kMaxHeads) return KATA_ERR_UNSUPPORTED;
-  // one CTA per segment, head and walk; at least 128 tokens to a segment (and up to 16 CTAs per split sequence,
-  // whose segments have at least 1024)
-  if (((long long)T / 128 + N) * H * 3 > 0x7fffffffll) return KATA_ERR_UNSUPPORTED;
+  // one CTA per segment, head and walk, and up to 16 for the scan of a split sequence, with at least 256 tokens to
+  // a segment
+  if (((long long)T / 256 * 16 + N) * H * 3 > 0x7fffffffll) return KATA_ERR_UNSUPPORTED;
   return KATA_OK;
 }
 

@@ -47,9 +47,9 @@ __device__ __forceinline__ bool seq_range(const int* __restrict__ cu, int n0, in
   return n >= N || (c0 >= 0 && c1 <= T && c0 <= c1);
 }
 
-// What find_segment counts: segments (an empty sequence is one empty segment)
-// or only the sequences that are cut into more than one.
-enum FindWhat { kSegments, kSplitSequences };
+// What find_segment counts: segments (an empty sequence is one empty segment),
+// only those of sequences that are cut into more than one, or these sequences.
+enum FindWhat { kSegments, kSplitSegments, kSplitSequences };
 
 // The target-th segment, or the first segment of the target-th split
 // sequence, when every sequence is cut into segments of L tokens.  Called by
@@ -67,7 +67,7 @@ __device__ __forceinline__ Segment find_segment(const int* __restrict__ cu, int 
     const int n = n0 + lane;
     const int segs = n < N ? max(1, (s1 - s0 + L - 1) / L) : 0;
     const int rec = segs > 1 ? segs : 0;
-    const int mine = what == kSegments ? segs : segs > 1 ? 1 : 0;
+    const int mine = what == kSegments ? segs : what == kSplitSegments ? rec : rec > 0 ? 1 : 0;
     int pc = mine, pr = rec;  // inclusive prefix sums
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -85,7 +85,7 @@ __device__ __forceinline__ Segment find_segment(const int* __restrict__ cu, int 
       r.s0 = __shfl_sync(0xffffffffu, s0, src);
       r.s1 = __shfl_sync(0xffffffffu, s1, src);
       r.n_seg = __shfl_sync(0xffffffffu, segs, src);
-      r.seg = what == kSegments ? target - (counted + __shfl_sync(0xffffffffu, pc - mine, src)) : 0;
+      r.seg = what == kSplitSequences ? 0 : target - (counted + __shfl_sync(0xffffffffu, pc - mine, src));
       r.rec = recs + __shfl_sync(0xffffffffu, pr - rec, src);
       r.t0 = r.s0 + r.seg * L;
       r.t1 = min(r.s1, r.t0 + L);

@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
   const WalkParams& w = p.w[wi];
   if (threadIdx.x < 32) {
     bool valid;
-    const Segment g = find_segment(p.cu, p.N, p.T, p.L, kSegments, item, threadIdx.x, valid);
+    const Segment g = find_segment(p.cu, p.N, p.T, p.L, kSum ? kSplitSegments : kSegments, item, threadIdx.x, valid);
     const int row = !kSum && g.seq >= 0 && (w.init || w.fin)
                         ? pool_row(p.slots, g.seq, p.n_slots, w.fin != nullptr, threadIdx.x, p.wc.status)
                         : -1;
@@ -813,8 +813,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
   }
   __syncthreads();
   if (found.seq < 0) return;
-  // nothing enters a segment from the one walked last, and nothing is cut in an uncut sequence
-  if (kSum && (found.n_seg == 1 || found.seg == (w.reverse ? 0 : found.n_seg - 1))) return;
+  // nothing enters a segment from the one walked last
+  if (kSum && found.seg == (w.reverse ? 0 : found.n_seg - 1)) return;
   if constexpr (DA != DB) {
     if (w.swapped) {
       if constexpr (kSum)
@@ -931,36 +931,38 @@ bool make_tmap(CUtensorMap* map, const void* base, int width, int H, int T, long
 }
 
 // How sequences are cut.  The lengths are on the device; the plan knows T, N,
-// the heads and the walks, and takes the length of segments that would be
-// best for sequences of equal length: a CTA per segment, waves of 148, a
-// chunk as the unit, about two more for a CTA's start and end, and where
-// anything is cut half as much again for the sums and a few chunks' time for
-// two more launches.  Shorter segments than kMinSegment or twice an even
-// share of the work are not taken, so that a call whose sequences differ is
-// cut only where one of them would outlast the rest.
+// the heads and the walks, and takes the length of segments that would be best
+// for sequences of equal length: a CTA per segment, waves of 148.  In units of
+// half a chunk's walk (measured: 1.6 us at d = dv = 128; a chunk's sum takes
+// one): kStart for a CTA's start and end, and where anything is cut kCut for
+// two more launches, with the sums.  Segments are not shorter than an even
+// share of the whole, so that of sequences that differ only those are cut that
+// would outlast the rest; and several short sequences (up to kUncut chunks
+// together) never, as even two more launches that find nothing to do cost
+// 6 us (a call of 1337 tokens in 5 sequences 37 us instead of 27).
 struct Plan {
   int L;              // tokens per segment, a multiple of 128
   int max_segments;   // of all sequences together
   int max_records;    // of split sequences
 };
 
-constexpr int kSMs = 148, kMinSegment = 8;
+constexpr int kSMs = 148, kMinSegment = 2, kUncut = 12, kStart = 4, kCut = 5;
 
 Plan make_plan(int T, int H, int N, int walks) {
   const long long heads = (long long)H * walks;
-  const long long len = ((long long)T / N + kChunk - 1) / kChunk;  // chunks of an even sequence
+  const long long chunks = ((long long)T + kChunk - 1) / kChunk;
+  const long long len = std::max(((long long)T / N + kChunk - 1) / kChunk, 1ll);  // chunks of an even sequence
   long long best = -1, k_best = 1;
-  for (long long k = std::max(len, 1ll); k >= 1; k = k > 64 ? k - k / 32 : k - 1) {
-    const long long segs = (std::max(len, 1ll) + k - 1) / k, waves = (segs * N * heads + kSMs - 1) / kSMs;
-    const long long cost = waves * (2 * k + 4) + (segs > 1 ? waves * k + 16 : 0);
+  for (long long k = len; k >= 1; k = k > 64 ? k - k / 32 : k - 1) {
+    const long long segs = (len + k - 1) / k, waves = (segs * N * heads + kSMs - 1) / kSMs;
+    const long long cost = waves * (2 * k + kStart) + (segs > 1 ? waves * k + kCut : 0);
     if (best < 0 || cost < best) {
       best = cost;
       k_best = k;
     }
   }
-  const long long chunks = ((long long)T + kChunk - 1) / kChunk;
-  const long long share = N > 1 ? 2 * ((chunks + N) * heads / kSMs) : 0;
-  const long long k = std::max(std::max(k_best, share), (long long)kMinSegment);
+  long long k = std::max(k_best, (long long)kMinSegment);
+  if (N > 1) k = std::max(k, chunks <= kUncut ? chunks : (chunks + N) * heads / kSMs);
   Plan pl;
   pl.L = (int)std::min(k * kChunk, 1ll << 30);
   pl.max_segments = N + T / pl.L;
@@ -981,7 +983,8 @@ cudaError_t launch(const Params& p, const Plan& pl, cudaStream_t st) {
   }
   e = cudaFuncSetAttribute(decay_walk_kernel<DA, DB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  decay_walk_kernel<DA, DB, true><<<grid, kSumThreads, bytes, st>>>(p);
+  decay_walk_kernel<DA, DB, true>
+      <<<dim3((unsigned)pl.max_records * p.H * p.n_walks), kSumThreads, bytes, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const dim3 scan(DA * DB / 4 / kScanThreads * (unsigned)std::min(p.N, p.T / pl.L) * p.H * p.n_walks);
   e = launch_pdl(decay_scan_kernel, scan, dim3(kScanThreads), 0, st, p, DA, DB);
