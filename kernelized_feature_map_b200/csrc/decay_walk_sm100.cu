@@ -89,23 +89,44 @@ struct Cfg {
   static constexpr int kA = kChunk * D1 * 2, kC = kChunk * D2 * 2;  // tile bytes
   static constexpr int kStage = 2 * kA + kC;                         // [A | B | C]
   static constexpr int kCopy = D1 * D2 * 2;
-  static constexpr int kFit = (226 * 1024 - kCopy) / kStage;
+  static constexpr int kFit = (224 * 1024 - kCopy) / kStage;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;                // 2 (128, 128) .. 4 (64, 64)
   static constexpr int offStage = 0;
   static constexpr int offCopy = kStages * kStage;
-  // the weights a^|y| of y = j - i, 0 on the side that is not kept, twice, the second
-  // time one entry on, so that the pair at any lane's j is aligned in one of them
-  static constexpr int kWeights = 178;  // 18 banks on: the two copies' reads share no bank
-  static constexpr int offWeight = offCopy + kCopy;
-  static constexpr int offBar = offWeight + 2 * kWeights * 4;
-  static constexpr int kBars = 4 * kStages + 11;
-  static constexpr int offMisc = offBar + kBars * 8;
-  static constexpr int kBytes = offMisc + 64 + 1024;    // + alignment slack
+  static constexpr int kBytes = offCopy + kCopy + 1024;  // + alignment slack
   static constexpr uint32_t colP = 0, colI = 128, colE = 128 + D2, colS = 128 + 2 * D2;
 };
-static_assert(Cfg<128, 128>::kStages >= 2 && Cfg<128, 128>::kBytes <= 227 * 1024, "shared memory");
-static_assert(Cfg<128, 64>::kBytes <= 227 * 1024 && Cfg<64, 128>::kBytes <= 227 * 1024, "shared memory");
-static_assert(Cfg<64, 64>::kBytes <= 227 * 1024, "shared memory");
+constexpr int kMaxStages = 4;
+
+// What a CTA sets up while it looks for its segment, the same for all widths.
+constexpr int kWeights = 178;  // 18 banks on: the two copies' reads share no bank
+struct Shared {
+  // the weights a^|y| of y = j - i, 0 on the side that is not kept, twice, the second
+  // time one entry on, so that the pair at any lane's j is aligned in one of them
+  float weight[2 * kWeights];
+  uint64_t full[kMaxStages];    // A and B landed (the sum: B and C)
+  uint64_t late[kMaxStages];    // C landed
+  uint64_t staged[kMaxStages];  // out in shared memory (256)
+  uint64_t done[kMaxStages];    // every product of the chunk complete
+  uint64_t scaled[kMaxStages];  // the sum's hi and lo written (128)
+  uint64_t p_full;              // P in TMEM
+  uint64_t w_full;              // W written (256)
+  uint64_t s_copied;            // S copied to shared memory (128)
+  uint64_t s_scaled;            // S scaled (128)
+  uint64_t a_done;              // A has met B and S: its tile takes lo
+  uint64_t hi_full;             // hi written, rows past the end cleared (256)
+  uint64_t lo_full;             // lo written (256)
+  uint64_t o_full;              // both accumulators of out complete
+  uint64_t o_free;              // and read (256)
+  uint64_t s_done;              // S advanced
+  uint64_t mma_done;            // every MMA issued has completed
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kMaxShared = 227 * 1024 - (int)sizeof(Shared) - 64;
+static_assert(Cfg<128, 128>::kStages >= 2 && Cfg<128, 128>::kBytes <= kMaxShared, "shared memory");
+static_assert(Cfg<128, 64>::kBytes <= kMaxShared && Cfg<64, 128>::kBytes <= kMaxShared, "shared memory");
+static_assert(Cfg<64, 64>::kBytes <= kMaxShared, "shared memory");
 
 struct Found {
   int seq, s0, s1, seg, n_seg, t0, t1, rec, row, resumed;
@@ -120,15 +141,14 @@ __device__ __forceinline__ uint32_t unit_offset(int rows, int r, int u) {
 // twenty of them, and written out in full they, with other loops unrolled, came
 // to 92 KB, more than an SM's instruction cache keeps.  The abort flag is the
 // CTA's; the limit and the status word are the call's.
-__shared__ int abort_flag;
-__device__ __forceinline__ bool wait_on(const WaitCtl& wc, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_on(const WaitCtl& wc, int* abort_flag, uint64_t* bar, uint32_t parity) {
   bool ok = mbar_test_wait(bar, parity);
   if (!ok) {
     const long long t0 = clock64();
     do {
-      if (*(volatile int*)&abort_flag) break;
+      if (*(volatile int*)abort_flag) break;
       if (clock64() - t0 >= wc.limit) {
-        abort_flag = 1;
+        *(volatile int*)abort_flag = 1;
         report_status(wc.status, kErrTimeout);
         break;
       }
@@ -239,29 +259,19 @@ __device__ __forceinline__ uint64_t key_desc(uint32_t tile) {
   return smem_desc(tile, D1 == 128 ? 16384u : 0u, 1024, kSw128);
 }
 
+// y of the first weight
+__device__ __forceinline__ int first_weight(bool reverse) { return reverse ? -32 : -128; }
+
 template <int D1, int D2>
-__device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem, const Found& f) {
+__device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8_t* smem, Shared& sh, const Found& f) {
   using C = Cfg<D1, D2>;
   constexpr int kStages = C::kStages;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::offBar);
-  uint64_t* full = bars;               // [kStages] A and B landed
-  uint64_t* late = full + kStages;     // [kStages] C landed
-  uint64_t* staged = late + kStages;   // [kStages] out in shared memory (256)
-  uint64_t* done = staged + kStages;   // [kStages] every product of the chunk complete
-  uint64_t* p_full = done + kStages;   // P in TMEM
-  uint64_t* w_full = p_full + 1;       // W written (256)
-  uint64_t* s_copied = w_full + 1;     // S copied to shared memory (128)
-  uint64_t* s_scaled = s_copied + 1;   // S scaled (128)
-  uint64_t* a_done = s_scaled + 1;     // A has met B and S: its tile takes lo
-  uint64_t* hi_full = a_done + 1;      // hi written, rows past the end cleared (256)
-  uint64_t* lo_full = hi_full + 1;     // lo written (256)
-  uint64_t* o_full = lo_full + 1;      // both accumulators of out complete
-  uint64_t* o_free = o_full + 1;       // and read (256)
-  uint64_t* s_done = o_free + 1;       // S advanced
-  uint64_t* mma_done = s_done + 1;     // every MMA issued has completed
-  float* weight = reinterpret_cast<float*>(smem + C::offWeight);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::offMisc);
-
+  uint64_t *full = sh.full, *late = sh.late, *staged = sh.staged, *done = sh.done;
+  uint64_t *p_full = &sh.p_full, *w_full = &sh.w_full, *s_copied = &sh.s_copied, *s_scaled = &sh.s_scaled;
+  uint64_t *a_done = &sh.a_done, *hi_full = &sh.hi_full, *lo_full = &sh.lo_full, *o_full = &sh.o_full;
+  uint64_t *o_free = &sh.o_free, *s_done = &sh.s_done, *mma_done = &sh.mma_done;
+  const float* weight = sh.weight;
+  const uint32_t tmem = sh.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool rev = w.reverse != 0;
   const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
@@ -289,46 +299,9 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + 2 * C::kA + x * 16384, &w.c, late + st, 64 * x, h, t);
   };
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(late + s, 1);
-      mbar_init(staged + s, 256);
-      mbar_init(done + s, 1);
-    }
-    mbar_init(p_full, 1);
-    mbar_init(w_full, 256);
-    mbar_init(s_copied, 128);
-    mbar_init(s_scaled, 128);
-    mbar_init(a_done, 1);
-    mbar_init(hi_full, 256);
-    mbar_init(lo_full, 256);
-    mbar_init(o_full, 1);
-    mbar_init(o_free, 256);
-    mbar_init(s_done, 1);
-    mbar_init(mma_done, 1);
-    abort_flag = 0;
-    fence_barrier_init();
-    fence_proxy_async_smem();
-#pragma unroll 1
-    for (int c = 0; c < min(kStages, n_chunks); ++c) {
-      load(c);
-      load_late(c);
-    }
-  }
-  const float g = used_log_decay(p.log_decay[h], p.wc.status);
-  const int y0 = rev ? -32 : -128;  // y of the first weight
-  if (threadIdx.x >= 64 && threadIdx.x < 64 + 2 * C::kWeights) {
-    const int x = (int)threadIdx.x - 64, y = y0 + x % C::kWeights + x / C::kWeights;
-    weight[x] = (rev ? y >= 0 : y <= 0) ? expf(g * fabsf((float)y)) : 0.f;
-  }
-  auto power = [&](int x) { return weight[rev ? 32 + x : 128 - x]; };  // a^x, x = 0 .. 128
-  if (warp == 1) tmem_alloc(tmem_holder, kTmemCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, bar, parity); };
+  const int y0 = first_weight(rev);
+  auto power = [&](int x) { return weight[rev ? x - y0 : -x - y0]; };  // a^x, x = 0 .. 128
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, &sh.abort, bar, parity); };
 
   if (warp < 4) {
     // --------------------------------------------------------------- S
@@ -352,14 +325,24 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
     if (split) griddep_wait();  // the scan's states
     if (n_chunks > 0) {
 #pragma unroll 1
-      for (int b = 0; b < D2 / 8; ++b) {
-        uint32_t r[8];
+      for (int b = 0; b < D2 / 16; ++b) {  // 16 columns' loads in flight
+        uint32_t r[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int j = 8 * b + e;
-          r[e] = src ? __float_as_uint(src[transposed ? j * D1 + l.row : l.row * D2 + j]) : 0u;
+        for (int e = 0; e < 16; ++e) r[e] = 0u;
+        if (src && transposed) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(src[(16 * b + e) * D1 + l.row]);
+        } else if (src) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 x = reinterpret_cast<const float4*>(src + l.row * D2 + 16 * b)[e];
+            r[4 * e] = __float_as_uint(x.x);
+            r[4 * e + 1] = __float_as_uint(x.y);
+            r[4 * e + 2] = __float_as_uint(x.z);
+            r[4 * e + 3] = __float_as_uint(x.w);
+          }
         }
-        tmem_st8(lane_base + 8 * b, r);
+        tmem_st16(lane_base + 16 * b, r);
       }
       tmem_wait_st();
     }
@@ -454,7 +437,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
           tmem_ld16(lane_base + C::colP + j0, r);
           tmem_wait_ld();
           const int at = j0 - i - y0;
-          const uint64_t* t = reinterpret_cast<const uint64_t*>(weight + (at & 1 ? C::kWeights + at - 1 : at));
+          const uint64_t* t = reinterpret_cast<const uint64_t*>(weight + (at & 1 ? kWeights + at - 1 : at));
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint64_t v = f32x2_mul(f32x2(r[2 * e], r[2 * e + 1]), t[e]);
@@ -519,12 +502,20 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
         }
       }
       if (!ok) break;
-      fence_proxy_async_smem();
+      if (n == kChunk) fence_proxy_async_smem();
       mbar_arrive(staged + c % kStages);
     }
   } else if (warp == 21) {
     // --------------------------------------------------------------- copies: tiles in, out
     int loaded = min(kStages, n_chunks), loaded_late = loaded;
+    if (lane == 0) {
+#pragma unroll 1
+      for (int c = 0; c < loaded; ++c) {
+        load(c);
+        load_late(c);
+      }
+    }
+    __syncwarp();
 #pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
@@ -647,24 +638,6 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
       mbar_arrive(lo_full);
     }
   }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
-  // rows of out outside every sequence
-  if (p.zero_outside) {
-    auto clear = [&](int t0, int t1) {
-      constexpr int kUnits = D2 / 8;
-      for (long long x = threadIdx.x; x < (long long)(t1 - t0) * kUnits; x += kThreads)
-        *reinterpret_cast<uint4*>(w.out + (t0 + x / kUnits) * w.out_stride + (long long)h * D2 + x % kUnits * 8) =
-            make_uint4(0u, 0u, 0u, 0u);
-    };
-    if (f.seq == 0 && f.seg == 0) clear(0, f.s0);
-    if (f.seq == p.N - 1 && f.seg == f.n_seg - 1) clear(f.s1, p.T);
-  }
 }
 
 // The sum of one segment of a sequence that is cut, from a zero state:
@@ -673,36 +646,18 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, uint8_t* smem,
 // chunk, so no product waits for another: bound by the loads of B and C.
 // Warps: 0 MMA, 1 TMA, 4-15 scale the keys in two or three groups, a chunk each.
 template <int D1, int D2>
-__device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t* smem, const Found& f) {
+__device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g, uint8_t* smem, Shared& sh,
+                            const Found& f) {
   using C = Cfg<D1, D2>;
   constexpr int kStages = C::kStages;
   // a stage always falls to the same group, so that no wait is ever a phase ahead
   constexpr int kGroups = kStages % 3 == 0 ? 3 : 2;
   static_assert(kStages % kGroups == 0, "groups of the scaling warps");
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::offBar);  // [kStages] tiles landed
-  uint64_t* empty = full + kStages;                                // [kStages] tiles read
-  uint64_t* scaled = empty + kStages;                              // [kStages] hi and lo written (128)
-  uint64_t* mma_done = scaled + kStages;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::offMisc);
+  uint64_t *full = sh.full, *empty = sh.done, *scaled = sh.scaled, *mma_done = &sh.mma_done;
+  const uint32_t tmem = sh.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 1);
-      mbar_init(scaled + s, 128);
-    }
-    mbar_init(mma_done, 1);
-    abort_flag = 0;
-    fence_barrier_init();
-  }
-  const float g = used_log_decay(p.log_decay[h], p.wc.status);
-  if (warp == 1) tmem_alloc(tmem_holder, kTmemCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, bar, parity); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, &sh.abort, bar, parity); };
   if (warp == 0) {
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);
     const uint32_t sStage = smem_u32(smem + C::offStage);
@@ -726,24 +681,22 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
     mma_commit_w(mma_done);
     mbar_wait_drain(mma_done, 0);
   } else if (warp == 1) {
-    {
-      int issued = 0;
+    int issued = 0;
 #pragma unroll 1
-      for (int c = 0; c < n_chunks; ++c, ++issued) {
-        const int st = c % kStages, t = f.t0 + c * kChunk;
-        if (!wait(empty + st, ((c / kStages) & 1) ^ 1)) break;
-        if (lane != 0) continue;
-        uint8_t* base = smem + C::offStage + st * C::kStage + C::kA;
-        mbar_arrive_expect_tx(full + st, C::kA + C::kC);
+    for (int c = 0; c < n_chunks; ++c, ++issued) {
+      const int st = c % kStages, t = f.t0 + c * kChunk;
+      if (!wait(empty + st, ((c / kStages) & 1) ^ 1)) break;
+      if (lane != 0) continue;
+      uint8_t* base = smem + C::offStage + st * C::kStage + C::kA;
+      mbar_arrive_expect_tx(full + st, C::kA + C::kC);
 #pragma unroll
-        for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + x * 16384, &w.b, full + st, 64 * x, h, t);
+      for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + x * 16384, &w.b, full + st, 64 * x, h, t);
 #pragma unroll
-        for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
-      }
-      // every copy that was issued ends before the CTA does
-#pragma unroll 1
-      for (int c = max(issued - kStages, 0); c < issued; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
+      for (int x = 0; x < D2 / 64; ++x) tma_load_3d(base + C::kA + x * 16384, &w.c, full + st, 64 * x, h, t);
     }
+    // every copy that was issued ends before the CTA does
+#pragma unroll 1
+    for (int c = max(issued - kStages, 0); c < issued; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
     __syncwarp();
   } else if (warp >= 4 && warp < 4 + 4 * kGroups) {
     const int j = (warp & 3) * 32 + lane;  // token of the chunk
@@ -754,7 +707,6 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
       const float fac =
           j < n ? w.s_key * expf(g * (float)(w.reverse ? t + j + 1 - f.t0 : f.t1 - 1 - t - j)) : 0.f;
       if (!wait(full + st, (c / kStages) & 1)) break;
-      uint32_t lo[D1 / 2];
       const KeyFactor kf(fac);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
@@ -778,12 +730,6 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, uint8_t
                   w.rec + ((long long)(f.rec + f.seg) * p.H + h) * (D1 * D2));
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
 }
 
 // DA, DB: the widths (d1, d2) of the walks; a `swapped` walk has them exchanged.
@@ -791,43 +737,93 @@ template <int DA, int DB, bool kSum>
 __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Shared sh;
   __shared__ Found found;
   if constexpr (kSum) griddep_launch_dependents();
   const int wi = blockIdx.x % p.n_walks, h = blockIdx.x / p.n_walks % p.H, item = blockIdx.x / p.n_walks / p.H;
   const WalkParams& w = p.w[wi];
-  if (threadIdx.x < 32) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float g = used_log_decay(p.log_decay[h], p.wc.status);
+  if (warp == 0) {
     bool valid;
-    const Segment g = find_segment(p.cu, p.N, p.T, p.L, kSum ? kSplitSegments : kSegments, item, threadIdx.x, valid);
-    const int row = !kSum && g.seq >= 0 && (w.init || w.fin)
-                        ? pool_row(p.slots, g.seq, p.n_slots, w.fin != nullptr, threadIdx.x, p.wc.status)
+    const Segment s = find_segment(p.cu, p.N, p.T, p.L, kSum ? kSplitSegments : kSegments, item, lane, valid);
+    const int row = !kSum && s.seq >= 0 && (w.init || w.fin)
+                        ? pool_row(p.slots, s.seq, p.n_slots, w.fin != nullptr, lane, p.wc.status)
                         : -1;
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       if (!valid) report_status(p.wc.status, kStatusInvalidArg);
-      found = Found{g.seq, g.s0, g.s1, g.seg, g.n_seg, g.t0, g.t1, g.rec, row,
-                    g.seq >= 0 && (!p.resume || p.resume[g.seq]) ? 1 : 0};
+      // nothing enters a segment from the one walked last
+      const bool idle = kSum && s.seg == (w.reverse ? 0 : s.n_seg - 1);
+      found = Found{idle ? -1 : s.seq, s.s0, s.s1, s.seg, s.n_seg, s.t0, s.t1, s.rec, row,
+                    s.seq >= 0 && (!p.resume || p.resume[s.seq]) ? 1 : 0};
+    }
+  } else if (warp == 1) {
+    tmem_alloc(&sh.tmem, kTmemCols);
+  } else if (warp == 2) {
+    if (lane == 0) {
+      for (int s = 0; s < kMaxStages; ++s) {
+        mbar_init(sh.full + s, 1);
+        mbar_init(sh.late + s, 1);
+        mbar_init(sh.staged + s, 256);
+        mbar_init(sh.done + s, 1);
+        mbar_init(sh.scaled + s, 128);
+      }
+      for (uint64_t* b : {&sh.p_full, &sh.a_done, &sh.o_full, &sh.s_done, &sh.mma_done}) mbar_init(b, 1);
+      for (uint64_t* b : {&sh.s_copied, &sh.s_scaled}) mbar_init(b, 128);
+      for (uint64_t* b : {&sh.w_full, &sh.hi_full, &sh.lo_full, &sh.o_free}) mbar_init(b, 256);
+      sh.abort = 0;
+      fence_barrier_init();
+      fence_proxy_async_smem();
+    }
+  } else if (warp == 3) {
+    if (lane == 0) {
       prefetch_tmap(&w.a);
       prefetch_tmap(&w.b);
       prefetch_tmap(&w.c);
       prefetch_tmap(&w.o);
     }
-  }
-  __syncthreads();
-  if (found.seq < 0) return;
-  // nothing enters a segment from the one walked last
-  if (kSum && found.seg == (w.reverse ? 0 : found.n_seg - 1)) return;
-  if constexpr (DA != DB) {
-    if (w.swapped) {
-      if constexpr (kSum)
-        sum_segment<DB, DA>(p, w, h, smem, found);
-      else
-        walk<DB, DA>(p, w, h, smem, found);
-      return;
+  } else if constexpr (!kSum) {
+    for (int x = threadIdx.x - 128; x < 2 * kWeights; x += kThreads - 128) {
+      const int y = first_weight(w.reverse) + x % kWeights + x / kWeights;
+      sh.weight[x] = (w.reverse ? y >= 0 : y <= 0) ? expf(g * fabsf((float)y)) : 0.f;
     }
   }
-  if constexpr (kSum)
-    sum_segment<DA, DB>(p, w, h, smem, found);
-  else
-    walk<DA, DB>(p, w, h, smem, found);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (found.seq >= 0) {
+    auto run = [&](auto d1, auto d2) {
+      if constexpr (kSum)
+        sum_segment<decltype(d1)::value, decltype(d2)::value>(p, w, h, g, smem, sh, found);
+      else
+        walk<decltype(d1)::value, decltype(d2)::value>(p, w, h, g, smem, sh, found);
+    };
+    using A = std::integral_constant<int, DA>;
+    using B = std::integral_constant<int, DB>;
+    if (DA != DB && w.swapped)
+      run(B(), A());
+    else
+      run(A(), B());
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(sh.tmem, kTmemCols);
+  }
+  // rows of out outside every sequence
+  if (!kSum && p.zero_outside && found.seq >= 0) {
+    const int units = (w.swapped ? DA : DB) / 8;
+    auto clear = [&](int t0, int t1) {
+#pragma unroll 1
+      for (int t = t0 + (int)threadIdx.x / units; t < t1; t += kThreads / units)
+        if ((int)threadIdx.x < kThreads / units * units)
+          *reinterpret_cast<uint4*>(w.out + t * w.out_stride + (long long)h * units * 8 + threadIdx.x % units * 8) =
+              make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (found.seq == 0 && found.seg == 0) clear(0, found.s0);
+    if (found.seq == p.N - 1 && found.seg == found.n_seg - 1) clear(found.s1, p.T);
+  }
 }
 
 // The sums of a split sequence's segments become the states that enter them:
