@@ -48,8 +48,9 @@ __device__ __forceinline__ bool seq_range(const int* __restrict__ cu, int n0, in
 }
 
 // What find_segment counts: segments (an empty sequence is one empty segment),
-// only those of sequences that are cut into more than one, or these sequences.
-enum FindWhat { kSegments, kSplitSegments, kSplitSequences };
+// only those of sequences that are cut into more than one, these sequences, or
+// those that are not cut.
+enum FindWhat { kSegments, kSplitSegments, kSplitSequences, kWholeSequences };
 
 // The target-th segment, or the first segment of the target-th split
 // sequence, when every sequence is cut into segments of L tokens.  Called by
@@ -67,7 +68,10 @@ __device__ __forceinline__ Segment find_segment(const int* __restrict__ cu, int 
     const int n = n0 + lane;
     const int segs = n < N ? max(1, (s1 - s0 + L - 1) / L) : 0;
     const int rec = segs > 1 ? segs : 0;
-    const int mine = what == kSegments ? segs : what == kSplitSegments ? rec : rec > 0 ? 1 : 0;
+    const int mine = what == kSegments        ? segs
+                     : what == kSplitSegments ? rec
+                     : what == kWholeSequences ? (segs == 1 ? 1 : 0)
+                                               : (rec > 0 ? 1 : 0);
     int pc = mine, pr = rec;  // inclusive prefix sums
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -85,7 +89,7 @@ __device__ __forceinline__ Segment find_segment(const int* __restrict__ cu, int 
       r.s0 = __shfl_sync(0xffffffffu, s0, src);
       r.s1 = __shfl_sync(0xffffffffu, s1, src);
       r.n_seg = __shfl_sync(0xffffffffu, segs, src);
-      r.seg = what == kSplitSequences ? 0 : target - (counted + __shfl_sync(0xffffffffu, pc - mine, src));
+      r.seg = what == kSplitSequences || what == kWholeSequences ? 0 : target - (counted + __shfl_sync(0xffffffffu, pc - mine, src));
       r.rec = recs + __shfl_sync(0xffffffffu, pr - rec, src);
       r.t0 = r.s0 + r.seg * L;
       r.t1 = min(r.s1, r.t0 + L);
@@ -98,17 +102,29 @@ __device__ __forceinline__ Segment find_segment(const int* __restrict__ cu, int 
   return r;
 }
 
+// Sequences that are not cut into segments of L tokens.  Called by a whole warp.
+__device__ __forceinline__ int count_whole(const int* __restrict__ cu, int N, int T, int L, int lane) {
+  int carry = 0, count = 0;
+  for (int n0 = 0; n0 < N; n0 += 32) {
+    int s0, s1;
+    seq_range(cu, n0, N, T, carry, lane, s0, s1);
+    count += __popc(__ballot_sync(0xffffffffu, n0 + lane < N && s1 - s0 <= L));
+    carry = __shfl_sync(0xffffffffu, s1, 31);
+  }
+  return count;
+}
+
 // Pool row named by index i of `idx` (null: i itself), or -1 where the index
 // is negative, out of range, or (unique) already named by an earlier one; the
 // latter two report.  Called by a whole warp, the same result in all lanes.
 __device__ __forceinline__ int pool_row(const int* __restrict__ idx, int i, int rows, bool unique, int lane,
                                         int* status) {
   if (!idx) return i;
-  const int s = idx[i];
+  const int s = idx[i], first = unique && lane < i ? idx[lane] : -1;  // both loads at once
   if (s < 0) return -1;
-  bool bad = s >= rows;
+  bool bad = s >= rows || first == s;
   if (unique)
-    for (int j = lane; j < i; j += 32) bad = bad || idx[j] == s;
+    for (int j = lane + 32; j < i; j += 32) bad = bad || idx[j] == s;
   if (__any_sync(0xffffffffu, bad)) {
     if (lane == 0) report_status(status, kStatusInvalidArg);
     return -1;

@@ -80,7 +80,7 @@ struct Params {
   const float* log_decay;
   const int* slots;
   const unsigned char* resume;
-  int n_walks, T, H, N, L, n_slots, zero_outside;
+  int n_walks, T, H, N, L, n_slots, zero_outside, folded;
   WaitCtl wc;
 };
 
@@ -111,6 +111,7 @@ struct Shared {
   uint64_t scaled[kMaxStages];  // the sum's hi and lo written (128)
   uint64_t p_full;              // P in TMEM
   uint64_t w_full;              // W written (256)
+  uint64_t s_init;              // the state that enters in TMEM (512)
   uint64_t s_copied;            // S copied to shared memory (128)
   uint64_t s_scaled;            // S scaled (128)
   uint64_t a_done;              // A has met B and S: its tile takes lo
@@ -188,20 +189,31 @@ struct StateLane {
   __device__ __forceinline__ bool own(int b) const { return 32 * b >= own0 && 32 * b < own1; }
 };
 
-// the state in TMEM to [d1][d2] fp32
+__device__ __forceinline__ void store_32b(void* to, const uint32_t* z) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(z[0]), "r"(z[1]), "r"(z[2]),
+               "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
+               : "memory");
+}
+
+// the state in TMEM to [d1][d2] fp32, whole sectors where it starts on one
 template <int D1, int D2>
 __device__ __forceinline__ void write_state(uint32_t lane_base, const StateLane<D1, D2>& l, float* dst) {
+  const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll 1
   for (int b = 0; b < D2 / 32; ++b) {
     uint32_t r[32];
     tmem_ld32(lane_base + 32 * b, r);
     tmem_wait_ld();
     if (!l.own(b)) continue;
-    float4* d4 = reinterpret_cast<float4*>(dst + (long long)l.row * D2 + 32 * b);
+    float* to = dst + l.row * D2 + 32 * b;
+    if (wide) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      d4[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
-                          __uint_as_float(r[4 * e + 3]));
+      for (int e = 0; e < 32; e += 8) store_32b(to + e, r + e);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<uint4*>(to + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+    }
   }
 }
 
@@ -259,6 +271,11 @@ __device__ __forceinline__ uint64_t key_desc(uint32_t tile) {
   return smem_desc(tile, D1 == 128 ? 16384u : 0u, 1024, kSw128);
 }
 
+// the segment that is walked last: no sum of it is needed, its record holds what enters the sequence
+__device__ __forceinline__ int last_walked(const WalkParams& w, const Found& f) {
+  return w.reverse ? 0 : f.n_seg - 1;
+}
+
 // y of the first weight
 __device__ __forceinline__ int first_weight(bool reverse) { return reverse ? -32 : -128; }
 
@@ -267,13 +284,13 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   using C = Cfg<D1, D2>;
   constexpr int kStages = C::kStages;
   uint64_t *full = sh.full, *late = sh.late, *staged = sh.staged, *done = sh.done;
-  uint64_t *p_full = &sh.p_full, *w_full = &sh.w_full, *s_copied = &sh.s_copied, *s_scaled = &sh.s_scaled;
+  uint64_t *s_init = &sh.s_init, *p_full = &sh.p_full, *w_full = &sh.w_full, *s_copied = &sh.s_copied, *s_scaled = &sh.s_scaled;
   uint64_t *a_done = &sh.a_done, *hi_full = &sh.hi_full, *lo_full = &sh.lo_full, *o_full = &sh.o_full;
   uint64_t *o_free = &sh.o_free, *s_done = &sh.s_done, *mma_done = &sh.mma_done;
   const float* weight = sh.weight;
   const uint32_t tmem = sh.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool rev = w.reverse != 0;
+  const bool rev = w.reverse != 0, split = f.n_seg > 1;
   const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
   // c-th chunk walked: its first token and its tokens
   auto chunk_t = [&](int c) { return f.t0 + (rev ? n_chunks - 1 - c : c) * kChunk; };
@@ -303,55 +320,78 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   auto power = [&](int x) { return weight[rev ? x - y0 : -x - y0]; };  // a^x, x = 0 .. 128
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, &sh.abort, bar, parity); };
 
+  // The state that enters, to TMEM, by the warps of W, out and B, a quarter of the
+  // columns each; 32 (16) columns' loads are in flight.  A cut sequence's segment
+  // starts from its scanned record, or sums those before it by itself, from the
+  // copy of what enters the sequence (which the last one may be overwriting).
+  constexpr int size = D1 * D2;
+  if (warp >= 4 && warp < 20 && n_chunks > 0) {
+    constexpr int kCols = D2 / 4;
+    const int m = warp % 4 * 32 + lane, row = m % D1, at = (warp / 4 - 1) * kCols;
+    const float* src = nullptr;
+    if (split)
+      src = w.rec + ((long long)(f.rec + (p.folded ? last_walked(w, f) : f.seg)) * p.H + h) * size;
+    else if (w.init && f.row >= 0 && f.resumed)
+      src = w.init + ((long long)f.row * p.H + h) * size;
+    const bool transposed = w.init_transposed && !split;
+    if (split) griddep_wait();  // the sums, scanned or not
+    float r[kCols];
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) r[e] = 0.f;
+    auto row_of = [&](const float* from, float (&x)[kCols]) {
+#pragma unroll
+      for (int e = 0; e < kCols; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(from + row * D2 + at + e);
+        x[e] = v.x;
+        x[e + 1] = v.y;
+        x[e + 2] = v.z;
+        x[e + 3] = v.w;
+      }
+    };
+    if (src && transposed) {
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) r[e] = src[(at + e) * D1 + row];
+    } else if (src) {
+      row_of(src, r);
+    }
+    if (split && p.folded) {
+      const int before = rev ? f.n_seg - 1 - f.seg : f.seg;
+#pragma unroll 1
+      for (int s = 0; s < before; ++s) {
+        const int seg = rev ? f.n_seg - 1 - s : s;
+        const float keep = expf(g * (float)min(p.L, f.s1 - f.s0 - seg * p.L));
+        float x[kCols];
+        row_of(w.rec + ((long long)(f.rec + seg) * p.H + h) * size, x);
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) r[e] = fmaf(keep, r[e], x[e]);
+      }
+    }
+    const uint32_t to = tmem + ((uint32_t)(warp % 4 * 32) << 16) + C::colS + at;
+#pragma unroll
+    for (int e = 0; e < kCols; e += 16) {
+      uint32_t z[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(r[e + k]);
+      tmem_st16(to + e, z);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(s_init);
+  }
+
   if (warp < 4) {
     // --------------------------------------------------------------- S
     const int quarter = warp;
     const StateLane<D1, D2> l(quarter, lane);
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colS;
     uint8_t* copy = smem + C::offCopy;
-    const long long size = (long long)D1 * D2;
-    const bool split = f.n_seg > 1;
-    const float* src = nullptr;
-    bool transposed = false;
-    if (split) {
-      src = w.rec + ((long long)(f.rec + f.seg) * p.H + h) * size;
-    } else if (w.init && f.row >= 0 && f.resumed) {
-      src = w.init + ((long long)f.row * p.H + h) * size;
-      transposed = w.init_transposed != 0;
-    }
     float* dst = w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1)
                      ? w.fin + ((long long)f.row * p.H + h) * size
                      : nullptr;
-    if (split) griddep_wait();  // the scan's states
-    if (n_chunks > 0) {
-#pragma unroll 1
-      for (int b = 0; b < D2 / 16; ++b) {  // 16 columns' loads in flight
-        uint32_t r[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) r[e] = 0u;
-        if (src && transposed) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(src[(16 * b + e) * D1 + l.row]);
-        } else if (src) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 x = reinterpret_cast<const float4*>(src + l.row * D2 + 16 * b)[e];
-            r[4 * e] = __float_as_uint(x.x);
-            r[4 * e + 1] = __float_as_uint(x.y);
-            r[4 * e + 2] = __float_as_uint(x.z);
-            r[4 * e + 3] = __float_as_uint(x.w);
-          }
-        }
-        tmem_st16(lane_base + 16 * b, r);
-      }
-      tmem_wait_st();
-    }
 #pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
-      if (c > 0) {
-        if (!wait(s_done, (c - 1) & 1)) break;
-        tc_fence_after();
-      }
+      if (!(c == 0 ? wait(s_init, 0) : wait(s_done, (c - 1) & 1))) break;
+      tc_fence_after();
       // The state before the chunk: first its copy, which A S waits for, then
       // itself scaled, for which the products onto it wait.
       uint32_t r[2][16];  // 16 columns, and the next 16 on their way
@@ -408,11 +448,11 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
         write_state(lane_base, l, dst);
       }
     } else if (dst) {  // an empty sequence leaves what it starts from
+      const float* src = w.init && f.resumed ? w.init + ((long long)f.row * p.H + h) * size : nullptr;
       for (int j = l.own0; j < l.own1; ++j)
-        dst[(long long)l.row * D2 + j] =
-            src ? src[transposed ? (long long)j * D1 + l.row : (long long)l.row * D2 + j] : 0.f;
+        dst[l.row * D2 + j] = src ? src[w.init_transposed ? j * D1 + l.row : l.row * D2 + j] : 0.f;
     }
-    if (!split) griddep_wait();  // a grid ends after those it was launched behind
+    griddep_wait();  // a grid ends after those it was launched behind
   } else if (warp < 12) {
     // --------------------------------------------------------------- W and out
     const int quarter = warp % 4, half = warp >= 8 ? 1 : 0;
@@ -732,6 +772,15 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
   }
 }
 
+// what enters the sequence, as [d1][d2], to the record of the segment walked last
+__device__ __noinline__ void copy_init(const WalkParams& w, const Found& f, int H, int h, int d1, int d2) {
+  const int size = d1 * d2;
+  const float* src = w.init && f.row >= 0 && f.resumed ? w.init + ((long long)f.row * H + h) * size : nullptr;
+  float* dst = w.rec + ((long long)(f.rec + f.seg) * H + h) * size;
+  for (int x = threadIdx.x; x < size; x += kSumThreads)
+    dst[x] = !src ? 0.f : src[w.init_transposed ? x % d2 * d1 + x / d2 : x];
+}
+
 // DA, DB: the widths (d1, d2) of the walks; a `swapped` walk has them exchanged.
 template <int DA, int DB, bool kSum>
 __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_kernel(const __grid_constant__ Params p) {
@@ -746,16 +795,21 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
   const float g = used_log_decay(p.log_decay[h], p.wc.status);
   if (warp == 0) {
     bool valid;
-    const Segment s = find_segment(p.cu, p.N, p.T, p.L, kSum ? kSplitSegments : kSegments, item, lane, valid);
-    const int row = !kSum && s.seq >= 0 && (w.init || w.fin)
+    // Sequences that are not cut first: they are walked while the others' sums are taken.
+    const int whole = kSum || p.L >= p.T ? 0 : count_whole(p.cu, p.N, p.T, p.L, lane);
+    const FindWhat what = !kSum && p.L >= p.T     ? kSegments
+                          : !kSum && item < whole ? kWholeSequences
+                                                  : kSplitSegments;
+    const Segment s = find_segment(p.cu, p.N, p.T, p.L, what, what == kSplitSegments ? item - whole : item, lane, valid);
+    const bool last = kSum && s.seg == (w.reverse ? 0 : s.n_seg - 1), states = !kSum || last;
+    const bool resumed = states && s.seq >= 0 && (!p.resume || p.resume[s.seq]);
+    const int row = states && s.seq >= 0 && (w.init || w.fin)
                         ? pool_row(p.slots, s.seq, p.n_slots, w.fin != nullptr, lane, p.wc.status)
                         : -1;
     if (lane == 0) {
       if (!valid) report_status(p.wc.status, kStatusInvalidArg);
-      // nothing enters a segment from the one walked last
-      const bool idle = kSum && s.seg == (w.reverse ? 0 : s.n_seg - 1);
-      found = Found{idle ? -1 : s.seq, s.s0, s.s1, s.seg, s.n_seg, s.t0, s.t1, s.rec, row,
-                    s.seq >= 0 && (!p.resume || p.resume[s.seq]) ? 1 : 0};
+      found = Found{s.seq, s.s0, s.s1, s.seg, s.n_seg, s.t0, s.t1, s.rec, row,
+                    resumed ? 1 : 0};
     }
   } else if (warp == 1) {
     tmem_alloc(&sh.tmem, kTmemCols);
@@ -770,6 +824,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
       }
       for (uint64_t* b : {&sh.p_full, &sh.a_done, &sh.o_full, &sh.s_done, &sh.mma_done}) mbar_init(b, 1);
       for (uint64_t* b : {&sh.s_copied, &sh.s_scaled}) mbar_init(b, 128);
+      mbar_init(&sh.s_init, 512);
       for (uint64_t* b : {&sh.w_full, &sh.hi_full, &sh.lo_full, &sh.o_free}) mbar_init(b, 256);
       sh.abort = 0;
       fence_barrier_init();
@@ -800,7 +855,9 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
     };
     using A = std::integral_constant<int, DA>;
     using B = std::integral_constant<int, DB>;
-    if (DA != DB && w.swapped)
+    if (kSum && found.seg == last_walked(w, found))
+      copy_init(w, found, p.H, h, w.swapped ? DB : DA, w.swapped ? DA : DB);
+    else if (DA != DB && w.swapped)
       run(B(), A());
     else
       run(A(), B());
@@ -942,7 +999,9 @@ struct Plan {
   int max_records;    // of split sequences
 };
 
-constexpr int kSMs = 148, kMinSegment = 2, kUncut = 12, kStart = 4, kCut = 5;
+// Up to kFold segments of a sequence a walk sums the records before its own
+// itself (each costs it about half a microsecond, the scan a launch of 7 us).
+constexpr int kSMs = 148, kMinSegment = 2, kUncut = 12, kStart = 4, kCut = 5, kFold = 16;
 
 Plan make_plan(int T, int H, int N, int walks) {
   const long long heads = (long long)H * walks;
@@ -982,6 +1041,7 @@ cudaError_t launch(const Params& p, const Plan& pl, cudaStream_t st) {
   decay_walk_kernel<DA, DB, true>
       <<<dim3((unsigned)pl.max_records * p.H * p.n_walks), kSumThreads, bytes, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.folded) return launch_pdl(decay_walk_kernel<DA, DB, false>, grid, dim3(kThreads), (size_t)bytes, st, p);
   const dim3 scan(DA * DB / 4 / kScanThreads * (unsigned)std::min(p.N, p.T / pl.L) * p.H * p.n_walks);
   e = launch_pdl(decay_scan_kernel, scan, dim3(kScanThreads), 0, st, p, DA, DB);
   if (e != cudaSuccess) return e;
@@ -1028,6 +1088,7 @@ cudaError_t launch_decay_walks(const DecayWalk* walks, int n, const DecayShape& 
   p.H = sh.H;
   p.N = sh.N;
   p.L = pl.L;
+  p.folded = sh.T / pl.L < kFold;
   p.n_slots = sh.n_slots;
   p.zero_outside = sh.zero_outside;
   p.wc = wc;
