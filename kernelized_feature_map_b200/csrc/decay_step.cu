@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kThreads) decay_step_kernel(const StepArgs a) 
   constexpr int kPasses = D / kRowsPerPass;
   __shared__ float sq[D], sk[D];
   __shared__ float4 red[kThreads / 32][kLanes];
+  griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slabs = a.dv / kSlab;
   const int slab = blockIdx.x % slabs, h = blockIdx.x / slabs % a.H, i = blockIdx.x / slabs / a.H;
@@ -119,14 +120,9 @@ cudaError_t launch_decay_step(const void* q, const void* k, const void* v, void*
   const StepArgs a{q, k, v, o, S, H, dv, n_slots, q_stride, k_stride, v_stride, o_stride, log_decay, scale, slots,
                    wc.status};
   const unsigned grid = (unsigned)n * H * (dv / kSlab);
-  if (dt == KATA_BF16) {
-    if (d == 64) decay_step_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, st>>>(a);
-    else decay_step_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(a);
-  } else {
-    if (d == 64) decay_step_kernel<float, 64><<<grid, kThreads, 0, st>>>(a);
-    else decay_step_kernel<float, 128><<<grid, kThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  auto run = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, st, a); };
+  if (dt == KATA_BF16) return d == 64 ? run(decay_step_kernel<__nv_bfloat16, 64>) : run(decay_step_kernel<__nv_bfloat16, 128>);
+  return d == 64 ? run(decay_step_kernel<float, 64>) : run(decay_step_kernel<float, 128>);
 }
 
 }  // namespace kata

@@ -32,9 +32,11 @@ __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / 
 // blocks the calling thread until that kernel has completed and its memory
 // operations are visible (it returns at once when there is no such
 // dependency), and griddep_launch_dependents() lets the next kernel start
-// launching before this one finishes.  Used only between the kernels of one
-// library call, whose data dependencies are known; the first kernel of a
-// call is launched normally, so it depends fully on earlier stream work.
+// launching before this one finishes.  Between the kernels of one library call
+// the data dependencies are known.  The first kernel of a call is launched
+// normally, or, where a launch's latency counts (a decode step, the state
+// cache), calls griddep_wait() in every thread before anything else: either
+// way it depends fully on earlier stream work.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -30,18 +30,41 @@ struct Q8 {
   static constexpr int kTileRows = kRowsPerPass * kUnroll;
 };
 
-// The integer nearest to x / s, ties to even, for |x| <= 127 s (1 + 2^-24) and
-// s >= 2^-126.  x * inv is within 2^-15 of the quotient, so q is at most one
-// off, and only next to a border; the remainder x - q s has no more than 24
-// bits (a multiple of half an ulp of s below s), so the fma gives it exactly
-// and its comparison with s / 2 decides.
-__device__ __forceinline__ int round_quotient(float x, float s, float inv) {
-  const float q = rintf(x * inv);
-  const float r = fmaf(-q, s, x);
-  const float h = 0.5f * s, a = fabsf(r);
-  int c = (int)q;
-  if (a > h || (a == h && (c & 1))) c += r > 0.f ? 1 : -1;
-  return c;
+// max / 127 rounded to nearest, for the scale of a row.  s0 = max * RN(1/127) is
+// within one unit of the quotient and max - 127 s0 is exact, so one more step
+// rounds correctly (P. Markstein, IBM J. Res. Dev. 34, 1990); a general division
+// in every lane cost a third of the kernel.
+__device__ __forceinline__ float row_scale(float max) {
+  constexpr float kInv = 1.f / 127.f;
+  const float s0 = max * kInv;
+  return fmaf(fmaf(-127.f, s0, max), kInv, s0);
+}
+
+// The integers nearest to x / s, ties to even, in the low bytes of t, for
+// |x| <= 127 s (1 + 2^-24) and s >= 2^-126.  Added to 1.5 2^23, x / s (times an
+// approximate 1 / s) is rounded to an integer q; the remainder x - q s has no
+// more than 24 bits, so the fma gives it exactly, and below s / 2 it proves q the
+// nearest.  Otherwise, next to a border, q is one off or x / s a tie.
+constexpr float kMagic = 12582912.f;
+struct Rounded {
+  float t, r;
+  __device__ __forceinline__ Rounded(float x, float s, float inv) {
+    t = fmaf(x, inv, kMagic);
+    r = fmaf(-(t - kMagic), s, x);
+  }
+  __device__ __forceinline__ void settle(float s) {
+    const float h = 0.5f * s, a = fabsf(r);
+    if (a > h || (a == h && (__float_as_uint(t) & 1u))) t += r > 0.f ? 1.f : -1.f;
+  }
+};
+
+// Largest of m over the kLanes lanes of this lane's row.
+template <int kLanes>
+__device__ __forceinline__ unsigned row_max(unsigned m) {
+  if constexpr (kLanes == 32) return __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
 }
 
 // The pair of this CTA: pool row and cache entry, false when it is skipped.
@@ -69,6 +92,7 @@ __global__ void __launch_bounds__(kThreads)
                           int n_entries, const int* __restrict__ slots, const int* __restrict__ entries,
                           long long rows, int* status) {
   using Q = Q8<DV>;
+  griddep_wait();
   int slot, entry;
   if (!find_pair(slots, n_slots, entries, n_entries, blockIdx.y, status, slot, entry)) return;
   const int sub = threadIdx.x % Q::kLanes;
@@ -80,25 +104,28 @@ __global__ void __launch_bounds__(kThreads)
     const long long r = row0 + u * Q::kRowsPerPass;
     x[u] = r < rows ? __ldcs(src + r * Q::kLanes + sub) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  char4* dst = reinterpret_cast<char4*>(cache + (long long)entry * rows * DV);
+  unsigned* dst = reinterpret_cast<unsigned*>(cache + (long long)entry * rows * DV);
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const long long r = row0 + u * Q::kRowsPerPass;
     // as unsigned integers the magnitudes order like the values, NaN above infinity
     unsigned m = max(max(__float_as_uint(fabsf(x[u].x)), __float_as_uint(fabsf(x[u].y))),
                      max(__float_as_uint(fabsf(x[u].z)), __float_as_uint(fabsf(x[u].w))));
+    m = row_max<Q::kLanes>(m);
+    float s = row_scale(__uint_as_float(m));
+    const bool held = m < 0x7f800000u && s >= FLT_MIN;
+    const float inv = __frcp_rn(held ? s : 1.f);
+    Rounded v[4] = {{x[u].x, s, inv}, {x[u].y, s, inv}, {x[u].z, s, inv}, {x[u].w, s, inv}};
+    const float worst = fmaxf(fmaxf(fabsf(v[0].r), fabsf(v[1].r)), fmaxf(fabsf(v[2].r), fabsf(v[3].r)));
+    if (__any_sync(0xffffffffu, worst >= 0.5f * s)) {
 #pragma unroll
-    for (int o = Q::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = __fdiv_rn(__uint_as_float(m), 127.f);
-    char4 c = make_char4(0, 0, 0, 0);
-    if (m >= 0x7f800000u) {
-      s = __uint_as_float(0x7fc00000u);
-    } else if (s < FLT_MIN) {
-      s = 0.f;
-    } else {
-      const float inv = __frcp_rn(s);
-      c = make_char4((signed char)round_quotient(x[u].x, s, inv), (signed char)round_quotient(x[u].y, s, inv),
-                     (signed char)round_quotient(x[u].z, s, inv), (signed char)round_quotient(x[u].w, s, inv));
+      for (int e = 0; e < 4; ++e) v[e].settle(s);
+    }
+    unsigned c = __byte_perm(__byte_perm(__float_as_uint(v[0].t), __float_as_uint(v[1].t), 0x0040),
+                             __byte_perm(__float_as_uint(v[2].t), __float_as_uint(v[3].t), 0x0040), 0x5410);
+    if (!held) {
+      c = 0u;
+      s = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : 0.f;
     }
     if (r < rows) {
       dst[r * Q::kLanes + sub] = c;
@@ -117,6 +144,7 @@ __global__ void __launch_bounds__(kThreads)
                          float* __restrict__ z, int n_slots, const int* __restrict__ entries,
                          const int* __restrict__ slots, long long rows, int* status) {
   using Q = Q8<DV>;
+  griddep_wait();
   int entry, slot;
   if (!find_pair(entries, n_entries, slots, n_slots, blockIdx.y, status, entry, slot)) return;
   const int sub = threadIdx.x % Q::kLanes;
@@ -154,9 +182,8 @@ cudaError_t launch_state_store_q8(const float* S, const float* z, int n_slots, s
                                   long long rows, int dv, const WaitCtl& wc, cudaStream_t st) {
   auto run = [&](auto width) {
     constexpr int DV = decltype(width)::value;
-    state_store_q8_kernel<DV><<<q8_grid<DV>(rows, n), kThreads, 0, st>>>(
-        S, z, n_slots, reinterpret_cast<int8_t*>(cache), scale, z_cache, n_entries, slots, entries, rows, wc.status);
-    return cudaGetLastError();
+    return launch_pdl(state_store_q8_kernel<DV>, q8_grid<DV>(rows, n), dim3(kThreads), 0, st, S, z, n_slots,
+                      reinterpret_cast<int8_t*>(cache), scale, z_cache, n_entries, slots, entries, rows, wc.status);
   };
   if (dv == 16) return run(std::integral_constant<int, 16>());
   if (dv == 64) return run(std::integral_constant<int, 64>());
@@ -168,10 +195,9 @@ cudaError_t launch_state_load_q8(const signed char* cache, const float* scale, c
                                  long long rows, int dv, const WaitCtl& wc, cudaStream_t st) {
   auto run = [&](auto width) {
     constexpr int DV = decltype(width)::value;
-    state_load_q8_kernel<DV><<<q8_grid<DV>(rows, n), kThreads, 0, st>>>(
-        reinterpret_cast<const int8_t*>(cache), scale, z_cache, n_entries, S, z, n_slots, entries, slots, rows,
-        wc.status);
-    return cudaGetLastError();
+    return launch_pdl(state_load_q8_kernel<DV>, q8_grid<DV>(rows, n), dim3(kThreads), 0, st,
+                      reinterpret_cast<const int8_t*>(cache), scale, z_cache, n_entries, S, z, n_slots, entries, slots,
+                      rows, wc.status);
   };
   if (dv == 16) return run(std::integral_constant<int, 16>());
   if (dv == 64) return run(std::integral_constant<int, 64>());
