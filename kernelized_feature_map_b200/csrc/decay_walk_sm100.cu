@@ -47,6 +47,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "decay_common.cuh"
 #include "kata_internal.h"
@@ -80,7 +81,7 @@ struct Params {
   const float* log_decay;
   const int* slots;
   const unsigned char* resume;
-  int n_walks, T, H, N, L, n_slots, zero_outside, folded;
+  int n_walks, T, H, N, L, n_slots, zero_outside, folded, max_records;
   WaitCtl wc;
 };
 
@@ -788,6 +789,7 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Shared sh;
   __shared__ Found found;
+  if (kSum || p.max_records == 0) griddep_wait();  // the first kernel of the call
   if constexpr (kSum) griddep_launch_dependents();
   const int wi = blockIdx.x % p.n_walks, h = blockIdx.x / p.n_walks % p.H, item = blockIdx.x / p.n_walks / p.H;
   const WalkParams& w = p.w[wi];
@@ -1025,27 +1027,35 @@ Plan make_plan(int T, int H, int N, int walks) {
   return pl;
 }
 
+// The kernel's dynamic shared memory, set once per context (it took 1 us of every call).
+template <int DA, int DB, bool kSum>
+cudaError_t allow_shared(int bytes) {
+  static std::atomic<void*> set{nullptr};
+  void* ctx = current_context();
+  if (ctx && set.load(std::memory_order_acquire) == ctx) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(decay_walk_kernel<DA, DB, kSum>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) set.store(current_context(), std::memory_order_release);
+  return e;
+}
+
 template <int DA, int DB>
 cudaError_t launch(const Params& p, const Plan& pl, cudaStream_t st) {
   constexpr int bytes = Cfg<DA, DB>::kBytes > Cfg<DB, DA>::kBytes ? Cfg<DA, DB>::kBytes : Cfg<DB, DA>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(decay_walk_kernel<DA, DB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       bytes);
+  cudaError_t e = allow_shared<DA, DB, false>(bytes);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)pl.max_segments * p.H * p.n_walks);
-  if (pl.max_records == 0) {
-    decay_walk_kernel<DA, DB, false><<<grid, kThreads, bytes, st>>>(p);
-    return cudaGetLastError();
-  }
-  e = cudaFuncSetAttribute(decay_walk_kernel<DA, DB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  auto walks = [&] { return launch_pdl(decay_walk_kernel<DA, DB, false>, grid, dim3(kThreads), (size_t)bytes, st, p); };
+  if (pl.max_records == 0) return walks();
+  if ((e = allow_shared<DA, DB, true>(bytes)) != cudaSuccess) return e;
+  e = launch_pdl(decay_walk_kernel<DA, DB, true>, dim3((unsigned)pl.max_records * p.H * p.n_walks), dim3(kSumThreads),
+                 (size_t)bytes, st, p);
   if (e != cudaSuccess) return e;
-  decay_walk_kernel<DA, DB, true>
-      <<<dim3((unsigned)pl.max_records * p.H * p.n_walks), kSumThreads, bytes, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.folded) return launch_pdl(decay_walk_kernel<DA, DB, false>, grid, dim3(kThreads), (size_t)bytes, st, p);
+  if (p.folded) return walks();
   const dim3 scan(DA * DB / 4 / kScanThreads * (unsigned)std::min(p.N, p.T / pl.L) * p.H * p.n_walks);
   e = launch_pdl(decay_scan_kernel, scan, dim3(kScanThreads), 0, st, p, DA, DB);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decay_walk_kernel<DA, DB, false>, grid, dim3(kThreads), (size_t)bytes, st, p);
+  return walks();
 }
 
 }  // namespace
@@ -1089,6 +1099,7 @@ cudaError_t launch_decay_walks(const DecayWalk* walks, int n, const DecayShape& 
   p.N = sh.N;
   p.L = pl.L;
   p.folded = sh.T / pl.L < kFold;
+  p.max_records = pl.max_records;
   p.n_slots = sh.n_slots;
   p.zero_outside = sh.zero_outside;
   p.wc = wc;
