@@ -139,6 +139,22 @@ __device__ __forceinline__ uint32_t unit_offset(int rows, int r, int u) {
   return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
 }
 
+// Shared memory by its 32-bit address: a store whose pointer may also be a global
+// one, as those of out, is compiled to a generic store, which takes twice as long.
+__device__ __forceinline__ void sts128(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t from) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from));
+  return v;
+}
+__device__ __forceinline__ uint64_t lds64(uint32_t from) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(from));
+  return v;
+}
+
 // Bounded wait as mbar_wait_w of sm100.cuh, in less code: a walk has more than
 // twenty of them, and written out in full they, with other loops unrolled, came
 // to 92 KB, more than an SM's instruction cache keeps.  The abort flag is the
@@ -239,11 +255,11 @@ struct KeyFactor {
 
 // One half of a row of D values, from its tile
 template <int D>
-__device__ __forceinline__ void split_half(const uint8_t* tile, int j, int half, const KeyFactor& f,
+__device__ __forceinline__ void split_half(uint32_t tile, int j, int half, const KeyFactor& f,
                                            uint32_t (&hi)[D / 4], uint32_t (&lo)[D / 4]) {
 #pragma unroll
   for (int u = 0; u < D / 16; ++u) {
-    const uint4 x = *reinterpret_cast<const uint4*>(tile + unit_offset(kChunk, j, half * (D / 16) + u));
+    const uint4 x = lds128(tile + unit_offset(kChunk, j, half * (D / 16) + u));
     hi[4 * u] = f.split(x.x, lo[4 * u]);
     hi[4 * u + 1] = f.split(x.y, lo[4 * u + 1]);
     hi[4 * u + 2] = f.split(x.z, lo[4 * u + 2]);
@@ -252,18 +268,17 @@ __device__ __forceinline__ void split_half(const uint8_t* tile, int j, int half,
 }
 // and to a tile
 template <int D>
-__device__ __forceinline__ void write_half(uint8_t* tile, int j, int half, const uint32_t (&x)[D / 4]) {
+__device__ __forceinline__ void write_half(uint32_t tile, int j, int half, const uint32_t (&x)[D / 4]) {
 #pragma unroll
   for (int u = 0; u < D / 16; ++u)
-    *reinterpret_cast<uint4*>(tile + unit_offset(kChunk, j, half * (D / 16) + u)) =
-        make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+    sts128(tile + unit_offset(kChunk, j, half * (D / 16) + u), x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
 }
 // a half row of zeros
 template <int D>
-__device__ __forceinline__ void clear_half(uint8_t* tile, int j, int half) {
+__device__ __forceinline__ void clear_half(uint32_t tile, int j, int half) {
 #pragma unroll
   for (int u = 0; u < D / 16; ++u)
-    *reinterpret_cast<uint4*>(tile + unit_offset(kChunk, j, half * (D / 16) + u)) = make_uint4(0u, 0u, 0u, 0u);
+    sts128(tile + unit_offset(kChunk, j, half * (D / 16) + u), 0u, 0u, 0u, 0u);
 }
 
 // descriptors of the state's products: scaled keys (M-major), and the C tile (N-major)
@@ -288,7 +303,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   uint64_t *s_init = &sh.s_init, *p_full = &sh.p_full, *w_full = &sh.w_full, *s_copied = &sh.s_copied, *s_scaled = &sh.s_scaled;
   uint64_t *a_done = &sh.a_done, *hi_full = &sh.hi_full, *lo_full = &sh.lo_full, *o_full = &sh.o_full;
   uint64_t *o_free = &sh.o_free, *s_done = &sh.s_done, *mma_done = &sh.mma_done;
-  const float* weight = sh.weight;
+  const uint32_t weight = smem_u32(sh.weight);
   const uint32_t tmem = sh.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool rev = w.reverse != 0, split = f.n_seg > 1;
@@ -318,7 +333,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   };
 
   const int y0 = first_weight(rev);
-  auto power = [&](int x) { return weight[rev ? x - y0 : -x - y0]; };  // a^x, x = 0 .. 128
+  auto power = [&](int x) { return sh.weight[rev ? x - y0 : -x - y0]; };  // a^x, x = 0 .. 128
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, &sh.abort, bar, parity); };
 
   // The state that enters, to TMEM, by the warps of W, out and B, a quarter of the
@@ -385,7 +400,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
     const int quarter = warp;
     const StateLane<D1, D2> l(quarter, lane);
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colS;
-    uint8_t* copy = smem + C::offCopy;
+    const uint32_t copy = smem_u32(smem + C::offCopy);
     float* dst = w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1)
                      ? w.fin + ((long long)f.row * p.H + h) * size
                      : nullptr;
@@ -403,7 +418,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             z[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]), __uint_as_float(x[8 * e + 2 * k + 1]));
-          *reinterpret_cast<uint4*>(copy + unit_offset(D1, l.row, at / 8 + e)) = make_uint4(z[0], z[1], z[2], z[3]);
+          sts128(copy + unit_offset(D1, l.row, at / 8 + e), z[0], z[1], z[2], z[3]);
         }
       };
       tmem_ld16(lane_base + l.own0, r[0]);
@@ -478,10 +493,10 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
           tmem_ld16(lane_base + C::colP + j0, r);
           tmem_wait_ld();
           const int at = j0 - i - y0;
-          const uint64_t* t = reinterpret_cast<const uint64_t*>(weight + (at & 1 ? kWeights + at - 1 : at));
+          const uint32_t t = weight + 4 * (at & 1 ? kWeights + at - 1 : at);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint64_t v = f32x2_mul(f32x2(r[2 * e], r[2 * e + 1]), t[e]);
+            const uint64_t v = f32x2_mul(f32x2(r[2 * e], r[2 * e + 1]), lds64(t + 8 * e));
             x[e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
           }
           // what a weight of 0 does not remove if it is NaN or infinite: beyond the
@@ -531,15 +546,16 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
         // through the C tile, once the last product has read it; a copy of a tile
         // that is not full would reach into the next sequence
         if (n == kChunk && at == half * (D2 / 2)) ok = wait(s_done, c & 1);
-        uint8_t* stage = smem + C::offStage + c % kStages * C::kStage + 2 * C::kA;
-        uint4* orow = reinterpret_cast<uint4*>(w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + at);
+        if (n == kChunk) {
+          const uint32_t stage = smem_u32(smem + C::offStage) + c % kStages * C::kStage + 2 * C::kA;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint4 v = make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
-          if (n == kChunk)
-            *reinterpret_cast<uint4*>(stage + unit_offset(kChunk, i, at / 8 + e)) = v;
-          else if (i < n)
-            orow[e] = v;
+          for (int e = 0; e < 4; ++e)
+            sts128(stage + unit_offset(kChunk, i, at / 8 + e), z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+        } else if (i < n) {
+          uint4* orow =
+              reinterpret_cast<uint4*>(w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) orow[e] = make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
         }
       }
       if (!ok) break;
@@ -659,7 +675,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages, n = chunk_n(c);
       const bool live = j < n;
-      uint8_t* tA = smem + C::offStage + st * C::kStage;
+      const uint32_t tA = smem_u32(smem + C::offStage) + st * C::kStage;
       const KeyFactor kf(live ? w.s_key * power(rev ? j + 1 : n - 1 - j) : 0.f);
       uint32_t hi[D1 / 4], lo[D1 / 4];
       if (!wait(full + st, (c / kStages) & 1)) break;
@@ -744,7 +760,7 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
 #pragma unroll 1
     for (int c = (warp >> 2) - 1; c < n_chunks; c += kGroups) {
       const int st = c % kStages, t = f.t0 + c * kChunk, n = min(kChunk, f.t1 - t);
-      uint8_t* tA = smem + C::offStage + st * C::kStage;
+      const uint32_t tA = smem_u32(smem + C::offStage) + st * C::kStage;
       const float fac =
           j < n ? w.s_key * expf(g * (float)(w.reverse ? t + j + 1 - f.t0 : f.t1 - 1 - t - j)) : 0.f;
       if (!wait(full + st, (c / kStages) & 1)) break;
