@@ -91,7 +91,10 @@ class KataAttentionLinearDecay(torch.autograd.Function):
 def kata_attention_linear_decay(q, k, v, log_decay, cu_seqlens=None, scale=1.0, S0=None, return_state=False):
     """Differentiable linear attention with a per-head decay over packed
     sequences, q,k [T,H,d], v [T,H,dv] (bf16); S0 [N,H,d,dv] fp32.  Returns o,
-    or (o, S_out) with return_state=True; gradients reach q, k, v and S0."""
+    or (o, S_out) with return_state=True; gradients reach q, k, v and S0.  To
+    capture the backward pass into a CUDA graph, release eager autograd graphs
+    of the same leaves first: torch ties a leaf's accumulation to the stream of
+    the first graph that is alive, and refuses the capture otherwise."""
     if isinstance(log_decay, torch.Tensor) and log_decay.requires_grad:
         raise ValueError("log_decay gets no gradient: pass log_decay.detach()")
     return KataAttentionLinearDecay.apply(q, k, v, log_decay, cu_seqlens, scale, S0, return_state)

@@ -176,3 +176,29 @@ def test_binding_requires_cuda_tensors():
                               torch.zeros(1, 1, 64))
     with pytest.raises(ValueError):
         K.kata_attention_linear_decay(x, x, x, g.requires_grad_())
+
+
+def test_plan_of_segments(L):
+    """Through the workspace: short and many even sequences are not cut, long ones with few heads are; the records of
+    a cut call are [segments, H, d, dv] fp32 for each walk."""
+    size = L.kata_fwd_linear_decay_workspace_size
+    assert size(75, 16, 64, 64, 1) == 0 and size(1337, 8, 64, 128, 5) == 0 and size(256, 1, 128, 128, 1) == 0
+    one = size(131072, 16, 128, 128, 1)
+    assert one > 0 and one % (16 * 128 * 128 * 4) == 0 and one // (16 * 128 * 128 * 4) <= 16
+    assert size(9000, 1, 64, 64, 1) // (64 * 64 * 4) > 16  # enough segments for the scan
+    assert L.kata_bwd_linear_decay_workspace_size(9000, 1, 64, 64, 1) >= 3 * 64 * 64 * 4
+    assert size(-1, 1, 64, 64, 1) == 0 and size(100, 1, 32, 64, 1) == 0
+
+
+def test_binding_refuses_host_tensors():
+    build.build()
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    g, S = torch.zeros(2), torch.zeros(1, 2, 64, 64)
+    for call in (lambda: K.kata_fwd_linear_decay(x, x, x, g), lambda: K.kata_bwd_linear_decay(x, x, x, x, g),
+                 lambda: K.kata_decode_step_linear_decay(x, x, x, S, g),
+                 lambda: K.kata_state_store_q8(S, S, S), lambda: K.kata_state_load_q8(S, S, S),
+                 lambda: K.kata_fwd_linear_decay(None, x, x, g)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        K.kata_attention_linear_decay(x, x, x, g.requires_grad_())
