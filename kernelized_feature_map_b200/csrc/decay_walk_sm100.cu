@@ -59,7 +59,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 704, kSumThreads = 512;
+constexpr int kThreads = 704, kSumThreads = 768;
 constexpr int kMaxWalks = 3;
 constexpr uint32_t kTmemCols = 512;
 
@@ -94,34 +94,47 @@ struct Cfg {
   static constexpr int kStages = kFit > 4 ? 4 : kFit;                // 2 (128, 128) .. 4 (64, 64)
   static constexpr int offStage = 0;
   static constexpr int offCopy = kStages * kStage;
-  static constexpr int kBytes = offCopy + kCopy + 1024;  // + alignment slack
-  static constexpr uint32_t colP = 0, colI = 128, colE = 128 + D2, colS = 128 + 2 * D2;
+  // the sum: stages [B | C], then lo and rest
+  static constexpr int kSumStage = kA + kC;
+  static constexpr int kSumStages = (224 * 1024 - 2 * kA) / kSumStage >= 4 ? 4 : 2;
+  static constexpr int offLo = kSumStages * kSumStage;
+  static constexpr int kBytes =
+      (offCopy + kCopy > offLo + 2 * kA ? offCopy + kCopy : offLo + 2 * kA) + 1024;  // + alignment slack
+  static constexpr uint32_t colP = 0, colE = 128, colU = 128 + D2, colS = 128 + 2 * D2;
+  static constexpr uint32_t colSumU = 0, colSumS = 2 * D2;  // the sum: two accumulators, and the sum
 };
 constexpr int kMaxStages = 4;
 
 // What a CTA sets up while it looks for its segment, the same for all widths.
 constexpr int kWeights = 178;  // 18 banks on: the two copies' reads share no bank
 struct Shared {
-  // the weights a^|y| of y = j - i, 0 on the side that is not kept, twice, the second
+  // s_intra times the weights a^|y| of y = j - i, 0 on the side that is not kept, twice, the second
   // time one entry on, so that the pair at any lane's j is aligned in one of them
   float weight[2 * kWeights];
   uint64_t full[kMaxStages];    // A and B landed (the sum: B and C)
   uint64_t late[kMaxStages];    // C landed
   uint64_t staged[kMaxStages];  // out in shared memory (256)
   uint64_t done[kMaxStages];    // every product of the chunk complete
-  uint64_t scaled[kMaxStages];  // the sum's hi and lo written (128)
+  uint64_t scaled[kMaxStages];  // the sum's scaled keys written (256)
+  uint64_t lo_free[2];          // the sum's lo and rest read, of even and odd chunks
   uint64_t p_full;              // P in TMEM
   uint64_t w_full;              // W written (256)
   uint64_t s_init;              // the state that enters in TMEM (512)
   uint64_t s_copied;            // S copied to shared memory (128)
-  uint64_t s_scaled;            // S scaled (128)
-  uint64_t a_done;              // A has met B and S: its tile takes lo
+  uint64_t a_done;              // A has met B and S: its tile takes lo, and A S can be scaled
+  uint64_t e_ready;             // A S scaled (128)
   uint64_t hi_full;             // hi written, rows past the end cleared (256)
   uint64_t lo_full;             // lo written (256)
-  uint64_t o_full;              // both accumulators of out complete
+  uint64_t rest_full;           // rest written (256)
+  uint64_t rest_done;           // rest has met C: its tile takes hi
+  uint64_t o_full;              // out complete
   uint64_t o_free;              // and read (256)
-  uint64_t s_done;              // S advanced
+  uint64_t u_done;              // the chunk's sum complete
+  uint64_t sum_done[2];         // the sum's chunk sums complete, of even and odd chunks
+  uint64_t sum_free[2];         // and read (128)
   uint64_t mma_done;            // every MMA issued has completed
+  float keep[2];                // a^128, its rounded value and what that leaves out
+  float keep_segment;           // a^L
   uint32_t tmem;
   int abort;
 };
@@ -203,7 +216,6 @@ struct StateLane {
       : row((quarter * 32 + lane) % D1),
         own0(D1 == 64 && quarter >= 2 ? D2 / 2 : 0),
         own1(D1 == 64 && quarter < 2 ? D2 / 2 : D2) {}
-  __device__ __forceinline__ bool own(int b) const { return 32 * b >= own0 && 32 * b < own1; }
 };
 
 __device__ __forceinline__ void store_32b(void* to, const uint32_t* z) {
@@ -212,66 +224,100 @@ __device__ __forceinline__ void store_32b(void* to, const uint32_t* z) {
                : "memory");
 }
 
-// the state in TMEM to [d1][d2] fp32, whole sectors where it starts on one
-template <int D1, int D2>
-__device__ __forceinline__ void write_state(uint32_t lane_base, const StateLane<D1, D2>& l, float* dst) {
-  const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
-#pragma unroll 1
-  for (int b = 0; b < D2 / 32; ++b) {
-    uint32_t r[32];
-    tmem_ld32(lane_base + 32 * b, r);
-    tmem_wait_ld();
-    if (!l.own(b)) continue;
-    float* to = dst + l.row * D2 + 32 * b;
-    if (wide) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) store_32b(to + e, r + e);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        *reinterpret_cast<uint4*>(to + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
-    }
+// 8 values, a whole sector where they start on one
+__device__ __forceinline__ void store_8(float* to, const uint32_t (&x)[8], bool wide) {
+  if (wide) {
+    store_32b(to, x);
+  } else {
+    *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(to + 4) = make_uint4(x[4], x[5], x[6], x[7]);
   }
 }
 
-// Key row j of a chunk of n tokens, scaled, as hi + lo.  The factor is taken as
-// f1 + f2 (error 2^-18): with hi = f1 k rounded, f1 k - hi is a bf16 value, and
-// lo is that and f2 k, rounded.  Rows past the end (another sequence's, or
-// nothing) count as zeros, and are cleared in the C tile.
+// D columns of TMEM times a factor of the lane: 16 at a time, and the next 16 on their way
+template <int D>
+__device__ __forceinline__ void scale_columns(uint32_t col, float factor) {
+  const uint64_t f2 = f32x2(__float_as_uint(factor), __float_as_uint(factor));
+  uint32_t r[2][16];
+  auto put = [&](uint32_t at, uint32_t (&x)[16]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint64_t v = f32x2_mul(f32x2(x[2 * k], x[2 * k + 1]), f2);
+      x[2 * k] = (uint32_t)v;
+      x[2 * k + 1] = (uint32_t)(v >> 32);
+    }
+    tmem_st16(at, x);
+  };
+  tmem_ld16(col, r[0]);
+#pragma unroll 1
+  for (int at = 0; at < D; at += 32) {
+    tmem_wait_ld();
+    tmem_ld16(col + at + 16, r[1]);
+    put(col + at, r[0]);
+    tmem_wait_ld();
+    if (at + 32 < D) tmem_ld16(col + at + 32, r[0]);
+    put(col + at + 16, r[1]);
+  }
+}
+
+// A key times its factor, f k, as the sum of three bf16 values: hi = f1 k with f1
+// the factor rounded, lo = (f1 k - hi) + f2 k with f2 what f1 leaves out (the
+// parenthesis is a bf16 value), and rest what these leave out, from the product
+// in fp32.  Up to 2^-25 of f k is lost, as in fp32 arithmetic; hi and lo alone
+// would lose 2^-17 (4e-6 of the state in the mean square).  Rows past the end
+// (another sequence's, or nothing) count as zeros, and are cleared in the tiles.
 struct KeyFactor {
   __nv_bfloat162 f1, f2;
-  __device__ __forceinline__ explicit KeyFactor(float f) {
-    const __nv_bfloat16 a = __float2bfloat16_rn(f), b = __float2bfloat16_rn(f - __bfloat162float(a));
+  uint64_t f;
+  __device__ __forceinline__ explicit KeyFactor(float x) {
+    const __nv_bfloat16 a = __float2bfloat16_rn(x), b = __float2bfloat16_rn(x - __bfloat162float(a));
     f1 = __halves2bfloat162(a, a);
     f2 = __halves2bfloat162(b, b);
+    f = f32x2(__float_as_uint(x), __float_as_uint(x));
   }
-  __device__ __forceinline__ uint32_t split(uint32_t k, uint32_t& lo) const {
-    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&k);
-    const __nv_bfloat162 hi = __hmul2(x, f1), l = __hfma2(x, f2, __hfma2(x, f1, __hneg2(hi)));
-    lo = *reinterpret_cast<const uint32_t*>(&l);
-    return *reinterpret_cast<const uint32_t*>(&hi);
+  static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t x) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&x);
+  }
+  static __device__ __forceinline__ uint32_t bits(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+  static __device__ __forceinline__ uint64_t wide(uint32_t x) { return f32x2(x << 16, x & 0xffff0000u); }
+  __device__ __forceinline__ uint32_t high(uint32_t k) const { return bits(__hmul2(pair(k), f1)); }
+  __device__ __forceinline__ uint32_t low(uint32_t k) const {
+    return bits(__hfma2(pair(k), f2, __hfma2(pair(k), f1, __hneg2(__hmul2(pair(k), f1)))));
+  }
+  __device__ __forceinline__ uint32_t rest(uint32_t k) const {
+    const uint64_t minus = f32x2(0xbf800000u, 0xbf800000u);
+    uint64_t d = f32x2_fma(wide(high(k)), minus, f32x2_mul(wide(k), f));
+    d = f32x2_fma(wide(low(k)), minus, d);
+    return pack_bf16x2(f32x2_lo(d), f32x2_hi(d));
   }
 };
 
-// One half of a row of D values, from its tile
+// One half of a row of D values from its tile
 template <int D>
-__device__ __forceinline__ void split_half(uint32_t tile, int j, int half, const KeyFactor& f,
-                                           uint32_t (&hi)[D / 4], uint32_t (&lo)[D / 4]) {
+__device__ __forceinline__ void read_half(uint32_t tile, int j, int half, uint32_t (&x)[D / 4]) {
 #pragma unroll
   for (int u = 0; u < D / 16; ++u) {
-    const uint4 x = lds128(tile + unit_offset(kChunk, j, half * (D / 16) + u));
-    hi[4 * u] = f.split(x.x, lo[4 * u]);
-    hi[4 * u + 1] = f.split(x.y, lo[4 * u + 1]);
-    hi[4 * u + 2] = f.split(x.z, lo[4 * u + 2]);
-    hi[4 * u + 3] = f.split(x.w, lo[4 * u + 3]);
+    const uint4 v = lds128(tile + unit_offset(kChunk, j, half * (D / 16) + u));
+    x[4 * u] = v.x;
+    x[4 * u + 1] = v.y;
+    x[4 * u + 2] = v.z;
+    x[4 * u + 3] = v.w;
   }
 }
-// and to a tile
-template <int D>
-__device__ __forceinline__ void write_half(uint32_t tile, int j, int half, const uint32_t (&x)[D / 4]) {
+// What is computed from x before and after this is computed twice, not kept in
+// registers (x, hi, lo and rest together are 128).
+template <int N>
+__device__ __forceinline__ void compute_again(uint32_t (&x)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) asm volatile("" : "+r"(x[e]));
+}
+// and, through a function of each pair, to one
+template <int D, typename F>
+__device__ __forceinline__ void write_half(uint32_t tile, int j, int half, const uint32_t (&x)[D / 4], F of) {
 #pragma unroll
   for (int u = 0; u < D / 16; ++u)
-    sts128(tile + unit_offset(kChunk, j, half * (D / 16) + u), x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+    sts128(tile + unit_offset(kChunk, j, half * (D / 16) + u), of(x[4 * u]), of(x[4 * u + 1]), of(x[4 * u + 2]),
+           of(x[4 * u + 3]));
 }
 // a half row of zeros
 template <int D>
@@ -300,9 +346,11 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   using C = Cfg<D1, D2>;
   constexpr int kStages = C::kStages;
   uint64_t *full = sh.full, *late = sh.late, *staged = sh.staged, *done = sh.done;
-  uint64_t *s_init = &sh.s_init, *p_full = &sh.p_full, *w_full = &sh.w_full, *s_copied = &sh.s_copied, *s_scaled = &sh.s_scaled;
-  uint64_t *a_done = &sh.a_done, *hi_full = &sh.hi_full, *lo_full = &sh.lo_full, *o_full = &sh.o_full;
-  uint64_t *o_free = &sh.o_free, *s_done = &sh.s_done, *mma_done = &sh.mma_done;
+  uint64_t *s_init = &sh.s_init, *p_full = &sh.p_full, *w_full = &sh.w_full, *s_copied = &sh.s_copied, *e_ready = &sh.e_ready;
+  uint64_t *a_done = &sh.a_done, *hi_full = &sh.hi_full, *rest_done = &sh.rest_done, *lo_full = &sh.lo_full;
+  uint64_t *rest_full = &sh.rest_full, *o_full = &sh.o_full;
+  uint64_t *o_free = &sh.o_free, *u_done = &sh.u_done, *mma_done = &sh.mma_done;
+  const bool precise = w.fin != nullptr;  // rest reaches the state only: out is rounded to 2^-9
   const uint32_t weight = smem_u32(sh.weight);
   const uint32_t tmem = sh.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -333,7 +381,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   };
 
   const int y0 = first_weight(rev);
-  auto power = [&](int x) { return sh.weight[rev ? x - y0 : -x - y0]; };  // a^x, x = 0 .. 128
+  auto power = [&](int x) { return expf(g * (float)x); };  // a^x
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, &sh.abort, bar, parity); };
 
   // The state that enters, to TMEM, by the warps of W, out and B, a quarter of the
@@ -375,7 +423,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
 #pragma unroll 1
       for (int s = 0; s < before; ++s) {
         const int seg = rev ? f.n_seg - 1 - s : s;
-        const float keep = expf(g * (float)min(p.L, f.s1 - f.s0 - seg * p.L));
+        const int tokens = min(p.L, f.s1 - f.s0 - seg * p.L);
+        const float keep = tokens == p.L ? sh.keep_segment : expf(g * (float)tokens);
         float x[kCols];
         row_of(w.rec + ((long long)(f.rec + seg) * p.H + h) * size, x);
 #pragma unroll
@@ -404,66 +453,79 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
     float* dst = w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1)
                      ? w.fin + ((long long)f.row * p.H + h) * size
                      : nullptr;
+    const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+    bool ok = n_chunks == 0 || wait(s_init, 0);
 #pragma unroll 1
-    for (int c = 0; c < n_chunks; ++c) {
-      if (!(c == 0 ? wait(s_init, 0) : wait(s_done, (c - 1) & 1))) break;
+    for (int c = 0; ok && c <= n_chunks && n_chunks > 0; ++c) {
+      // The state before chunk c (c = n_chunks: the one that leaves): a^n S + U of
+      // the chunk before, added in fp32 (the tensor core's accumulation truncates:
+      // onto S it would cost 6e-7 of it every chunk).  8 columns at a time, and the
+      // next 8 on their way.
+      float k0 = 1.f, k1 = 0.f;
+      const bool add = c > 0, last = c == n_chunks;
+      if (add) {
+        if (!wait(u_done, (c - 1) & 1)) break;
+        if (last && !dst) break;
+        const int n = chunk_n(c - 1);
+        k0 = n == kChunk ? sh.keep[0] : power(n);
+        k1 = n == kChunk ? sh.keep[1] : 0.f;
+      }
       tc_fence_after();
-      // The state before the chunk: first its copy, which A S waits for, then
-      // itself scaled, for which the products onto it wait.
-      uint32_t r[2][16];  // 16 columns, and the next 16 on their way
-      auto put_copy = [&](int at, const uint32_t (&x)[16]) {
+      const uint64_t keep = f32x2(__float_as_uint(k0), __float_as_uint(k0));
+      const uint64_t more = f32x2(__float_as_uint(k1), __float_as_uint(k1));
+      uint32_t r[2][8], u[2][8];
+      auto fetch = [&](int at, int i) {
+        tmem_ld8(lane_base + at, r[i]);
+        tmem_ld8(lane_base - C::colS + C::colU + at, u[i]);  // before the first chunk: not used
+      };
+      auto step = [&](int at, int i) {
+        if (add) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t x = f32x2(r[i][2 * k], r[i][2 * k + 1]);
+            const uint64_t v = f32x2_fma(x, keep, f32x2_fma(x, more, f32x2(u[i][2 * k], u[i][2 * k + 1])));
+            r[i][2 * k] = (uint32_t)v;
+            r[i][2 * k + 1] = (uint32_t)(v >> 32);
+          }
+          if (!last) tmem_st8(lane_base + at, r[i]);
+        }
+        if (at < l.own0 || at >= l.own1) return;
+        if (last) {
+          store_8(dst + l.row * D2 + at, r[i], wide);
+        } else {
           uint32_t z[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            z[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]), __uint_as_float(x[8 * e + 2 * k + 1]));
-          sts128(copy + unit_offset(D1, l.row, at / 8 + e), z[0], z[1], z[2], z[3]);
+            z[k] = pack_bf16x2(__uint_as_float(r[i][2 * k]), __uint_as_float(r[i][2 * k + 1]));
+          sts128(copy + unit_offset(D1, l.row, at / 8), z[0], z[1], z[2], z[3]);
         }
       };
-      tmem_ld16(lane_base + l.own0, r[0]);
+      fetch(0, 0);
 #pragma unroll 1
-      for (int at = l.own0; at < l.own1; at += 32) {
+      for (int at = 0; at < D2; at += 16) {
         tmem_wait_ld();
-        tmem_ld16(lane_base + at + 16, r[1]);
-        put_copy(at, r[0]);
+        fetch(at + 8, 1);
+        step(at, 0);
         tmem_wait_ld();
-        if (at + 32 < l.own1) tmem_ld16(lane_base + at + 32, r[0]);
-        put_copy(at + 16, r[1]);
+        if (at + 16 < D2) fetch(at + 16, 0);
+        step(at + 8, 1);
       }
+      if (last) break;
+      tmem_wait_st();
       fence_proxy_async_smem();
+      tc_fence_before();
       mbar_arrive(s_copied);
-      const uint32_t f0 = __float_as_uint(power(chunk_n(c)));
-      const uint64_t keep = f32x2(f0, f0);
-      auto put_scaled = [&](int at, uint32_t (&x)[16]) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t v = f32x2_mul(f32x2(x[2 * k], x[2 * k + 1]), keep);
-          x[2 * k] = (uint32_t)v;
-          x[2 * k + 1] = (uint32_t)(v >> 32);
-        }
-        tmem_st16(lane_base + at, x);
-      };
-      tmem_ld16(lane_base, r[0]);
-#pragma unroll 1
-      for (int at = 0; at < D2; at += 32) {
-        tmem_wait_ld();
-        tmem_ld16(lane_base + at + 16, r[1]);
-        put_scaled(at, r[0]);
-        tmem_wait_ld();
-        if (at + 32 < D2) tmem_ld16(lane_base + at + 32, r[0]);
-        put_scaled(at + 16, r[1]);
-      }
+      // A S times a^reach: the product of W and C is added to it
+      const int i = quarter * 32 + lane, n = chunk_n(c);
+      const float reach = w.s_inter * power(rev ? max(n - 1 - i, 0) : i + 1);
+      if (!wait(a_done, c & 1)) break;
+      tc_fence_after();
+      scale_columns<D2>(lane_base - C::colS + C::colE, reach);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(s_scaled);
+      mbar_arrive(e_ready);
     }
-    if (n_chunks > 0) {
-      if (wait(s_done, (n_chunks - 1) & 1) && dst) {
-        tc_fence_after();
-        write_state(lane_base, l, dst);
-      }
-    } else if (dst) {  // an empty sequence leaves what it starts from
+    if (n_chunks == 0 && dst) {  // an empty sequence leaves what it starts from
       const float* src = w.init && f.resumed ? w.init + ((long long)f.row * p.H + h) * size : nullptr;
       for (int j = l.own0; j < l.own1; ++j)
         dst[l.row * D2 + j] = src ? src[w.init_transposed ? j * D1 + l.row : l.row * D2 + j] : 0.f;
@@ -514,38 +576,22 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(w_full);
-      // out = s_intra W C + s_inter a^reach A S
-      const uint32_t f0 = __float_as_uint(w.s_intra), f1 = __float_as_uint(w.s_inter * power(rev ? max(n - 1 - i, 0) : i + 1));
-      const uint64_t intra = f32x2(f0, f0), reach = f32x2(f1, f1);
+      // out, through the C tile, which every product has read by now; a copy of a
+      // tile that is not full would reach into the next sequence
       if (!wait(o_full, c & 1)) break;
       tc_fence_after();
-      bool ok = true;
 #pragma unroll 1
       for (int at = half * (D2 / 2); at < (half + 1) * (D2 / 2); at += 32) {
-        uint32_t z[16], x[2][8], y[2][8];
-        tmem_ld8(lane_base + C::colI + at, x[0]);
-        tmem_ld8(lane_base + C::colE + at, y[0]);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {  // 8 columns, and the next 8 on their way
-          tmem_wait_ld();
-          if (b + 1 < 4) {
-            tmem_ld8(lane_base + C::colI + at + 8 * (b + 1), x[(b + 1) & 1]);
-            tmem_ld8(lane_base + C::colE + at + 8 * (b + 1), y[(b + 1) & 1]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint64_t v = f32x2_fma(reach, f32x2(y[b & 1][2 * e], y[b & 1][2 * e + 1]),
-                                         f32x2_mul(intra, f32x2(x[b & 1][2 * e], x[b & 1][2 * e + 1])));
-            z[4 * b + e] = pack_bf16x2(f32x2_lo(v), f32x2_hi(v));
-          }
-        }
+        uint32_t x[32];
+        tmem_ld32(lane_base + C::colE + at, x);
+        tmem_wait_ld();
         if (at + 32 == (half + 1) * (D2 / 2)) {
           tc_fence_before();
           mbar_arrive(o_free);
         }
-        // through the C tile, once the last product has read it; a copy of a tile
-        // that is not full would reach into the next sequence
-        if (n == kChunk && at == half * (D2 / 2)) ok = wait(s_done, c & 1);
+        uint32_t z[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
         if (n == kChunk) {
           const uint32_t stage = smem_u32(smem + C::offStage) + c % kStages * C::kStage + 2 * C::kA;
 #pragma unroll
@@ -558,7 +604,6 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
           for (int e = 0; e < 4; ++e) orow[e] = make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
         }
       }
-      if (!ok) break;
       if (n == kChunk) fence_proxy_async_smem();
       mbar_arrive(staged + c % kStages);
     }
@@ -614,10 +659,21 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
       const uint32_t sA = sStage + st * C::kStage, sB = sA + C::kA, sC = sB + C::kA;
-      const uint64_t dA = smem_desc(sA, 16, 1024, kSw128), dC = smem_desc(sC, 16384, 1024, kSw128);
+      const uint64_t dA = smem_desc(sA, 16, 1024, kSw128), dB = smem_desc(sB, 16, 1024, kSw128);
+      const uint64_t dC = smem_desc(sC, 16384, 1024, kSw128);
+      const uint64_t kB = key_desc<D1>(sB), kA = key_desc<D1>(sA);
+      // U (+)= K^T C, K scaled keys in the B or the A tile
+      auto add_keys = [&](uint64_t keys, bool first, uint64_t* done) {
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < kChunk / 16; ++ks)
+            mma_ss(tmem + C::colU, desc_add(keys, ks * 2048), desc_add(dC, ks * 2048), id_s, !first || ks > 0);
+          if (done) mma_commit(done);
+        }
+        __syncwarp();
+      };
       if (!wait(full + st, (c / kStages) & 1)) break;
       tc_fence_after();
-      const uint64_t dB = smem_desc(sB, 16, 1024, kSw128);
       // over W of the chunk before only after its product, which was issued before
       if (elect_one()) {
 #pragma unroll
@@ -627,6 +683,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
         }
         mma_commit(p_full);
       }
+      __syncwarp();
+      // the copy of S, and with it U read
       if (!wait(s_copied, c & 1)) break;
       if (c > 0 && !wait(o_free, (c - 1) & 1)) break;
       tc_fence_after();
@@ -634,36 +692,34 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
 #pragma unroll
         for (int ks = 0; ks < D1 / 16; ++ks)
           mma_ss(tmem + C::colE, desc_add(dA, (ks >> 2) * 16384 + (ks & 3) * 32), desc_add(dcopy, ks * 2048), id_o,
-                   ks > 0);
+                 ks > 0);
         mma_commit(a_done);
       }
-      if (!wait(s_scaled, c & 1)) break;
-      if (!wait(hi_full, c & 1)) break;
+      __syncwarp();
+      // smallest first: what the accumulation truncates is a part of what is there
       if (!wait(late + st, (c / kStages) & 1)) break;
-      tc_fence_after();
-      const uint64_t dHi = key_desc<D1>(sB), dLo = key_desc<D1>(sA);
-      if (elect_one()) {
-#pragma unroll
-        for (int ks = 0; ks < kChunk / 16; ++ks)
-          mma_ss(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+      if (precise) {
+        if (!wait(rest_full, c & 1)) break;
+        tc_fence_after();
+        add_keys(kB, true, rest_done);
       }
+      if (!wait(lo_full, c & 1)) break;
+      tc_fence_after();
+      add_keys(kA, !precise, nullptr);
+      if (!wait(hi_full, c & 1)) break;
+      tc_fence_after();
+      add_keys(kB, false, u_done);
       if (!wait(w_full, c & 1)) break;
+      if (!wait(e_ready, c & 1)) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < kChunk / 16; ++ks)  // keys 16 ks ..: at the start of the 32 columns they came from
-          mma_ts(tmem + C::colI, tmem + C::colP + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dC, ks * 2048), id_o, ks > 0);
+          mma_ts(tmem + C::colE, tmem + C::colP + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dC, ks * 2048), id_o, 1);
         mma_commit(o_full);
-      }
-      if (!wait(lo_full, c & 1)) break;
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int ks = 0; ks < kChunk / 16; ++ks)
-          mma_ss(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
-        mma_commit(s_done);
         mma_commit(done + st);
       }
+      __syncwarp();
     }
     // every MMA that was issued ends before the CTA does
     mma_commit_w(mma_done);
@@ -677,22 +733,30 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       const bool live = j < n;
       const uint32_t tA = smem_u32(smem + C::offStage) + st * C::kStage;
       const KeyFactor kf(live ? w.s_key * power(rev ? j + 1 : n - 1 - j) : 0.f);
-      uint32_t hi[D1 / 4], lo[D1 / 4];
+      uint32_t x[D1 / 4];
       if (!wait(full + st, (c / kStages) & 1)) break;
       if (n < kChunk && !wait(late + st, (c / kStages) & 1)) break;
       if (!live) {  // of P only what W drops comes from these rows
         clear_half<D1>(tA + C::kA, j, half);
         clear_half<D2>(tA + 2 * C::kA, j, half);
       }
-      split_half<D1>(tA + C::kA, j, half, kf, hi, lo);
+      read_half<D1>(tA + C::kA, j, half, x);
       if (!wait(p_full, c & 1)) break;
-      write_half<D1>(tA + C::kA, j, half, hi);
-      fence_proxy_async_smem();
-      mbar_arrive(hi_full);
+      if (precise) {
+        write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.rest(k); });
+        fence_proxy_async_smem();
+        mbar_arrive(rest_full);
+        compute_again(x);
+      }
       if (!wait(a_done, c & 1)) break;
-      write_half<D1>(tA, j, half, lo);
+      write_half<D1>(tA, j, half, x, [&](uint32_t k) { return kf.low(k); });
       fence_proxy_async_smem();
       mbar_arrive(lo_full);
+      compute_again(x);
+      if (precise && !wait(rest_done, c & 1)) break;
+      write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.high(k); });
+      fence_proxy_async_smem();
+      mbar_arrive(hi_full);
     }
   }
 }
@@ -701,39 +765,46 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
 //   sum_t a^(tokens of the segment after t) B_t C_t^T   (backwards: a^(tokens before t, and t))
 // With each key scaled for the segment's end nothing is carried from chunk to
 // chunk, so no product waits for another: bound by the loads of B and C.
-// Warps: 0 MMA, 1 TMA, 4-15 scale the keys in two or three groups, a chunk each.
+// Warps: 0 MMA, 1 TMA, 4-19 scale the keys in two groups, a chunk each, 20-23
+// add the chunks' sums.
 template <int D1, int D2>
 __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g, uint8_t* smem, Shared& sh,
                             const Found& f) {
   using C = Cfg<D1, D2>;
-  constexpr int kStages = C::kStages;
-  // a stage always falls to the same group, so that no wait is ever a phase ahead
-  constexpr int kGroups = kStages % 3 == 0 ? 3 : 2;
-  static_assert(kStages % kGroups == 0, "groups of the scaling warps");
-  uint64_t *full = sh.full, *empty = sh.done, *scaled = sh.scaled, *mma_done = &sh.mma_done;
+  constexpr int kStages = C::kSumStages;
+  uint64_t *full = sh.full, *empty = sh.done, *scaled = sh.scaled, *lo_free = sh.lo_free, *mma_done = &sh.mma_done;
   const uint32_t tmem = sh.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
+  const uint32_t sStage = smem_u32(smem), sLo = sStage + C::offLo, sRest = sLo + C::kA;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, &sh.abort, bar, parity); };
   if (warp == 0) {
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);
-    const uint32_t sStage = smem_u32(smem + C::offStage);
 #pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
-      const uint32_t sA = sStage + st * C::kStage;
-      const uint64_t dLo = key_desc<D1>(sA), dHi = key_desc<D1>(sA + C::kA);
-      const uint64_t dC = smem_desc(sA + 2 * C::kA, 16384, 1024, kSw128);
+      const uint32_t sB = sStage + st * C::kSumStage;
+      const uint64_t dC = smem_desc(sB + C::kA, 16384, 1024, kSw128);
       if (!wait(full + st, (c / kStages) & 1)) break;
       if (!wait(scaled + st, (c / kStages) & 1)) break;
       tc_fence_after();
+      if (c > 1 && !wait(sh.sum_free + (c & 1), ((c >> 1) - 1) & 1)) break;
+      tc_fence_after();
+      // smallest first, into an accumulator of the chunk's own
+#pragma unroll 1
+      for (int part = 0; part < 3; ++part) {
+        const uint64_t dK = key_desc<D1>(part == 0 ? sRest : part == 1 ? sLo : sB);
+        if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks)
-        mma_ss_w(tmem + C::colS, desc_add(dHi, ks * 2048), desc_add(dC, ks * 2048), id_s, c > 0 || ks > 0);
-#pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks)
-        mma_ss_w(tmem + C::colS, desc_add(dLo, ks * 2048), desc_add(dC, ks * 2048), id_s, 1);
+          for (int ks = 0; ks < kChunk / 16; ++ks)
+            mma_ss(tmem + C::colSumU + (c & 1) * D2, desc_add(dK, ks * 2048), desc_add(dC, ks * 2048), id_s,
+                   part + ks > 0);
+        }
+        __syncwarp();
+      }
+      mma_commit_w(sh.sum_done + (c & 1));
       mma_commit_w(empty + st);
+      mma_commit_w(lo_free + (c & 1));
     }
     mma_commit_w(mma_done);
     mbar_wait_drain(mma_done, 0);
@@ -744,8 +815,8 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
       const int st = c % kStages, t = f.t0 + c * kChunk;
       if (!wait(empty + st, ((c / kStages) & 1) ^ 1)) break;
       if (lane != 0) continue;
-      uint8_t* base = smem + C::offStage + st * C::kStage + C::kA;
-      mbar_arrive_expect_tx(full + st, C::kA + C::kC);
+      uint8_t* base = smem + st * C::kSumStage;
+      mbar_arrive_expect_tx(full + st, C::kSumStage);
 #pragma unroll
       for (int x = 0; x < D1 / 64; ++x) tma_load_3d(base + x * 16384, &w.b, full + st, 64 * x, h, t);
 #pragma unroll
@@ -755,36 +826,64 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
 #pragma unroll 1
     for (int c = max(issued - kStages, 0); c < issued; ++c) mbar_wait_drain(full + c % kStages, (c / kStages) & 1);
     __syncwarp();
-  } else if (warp >= 4 && warp < 4 + 4 * kGroups) {
-    const int j = (warp & 3) * 32 + lane;  // token of the chunk
+  } else if (warp >= 20) {
+    // the chunks' sums, added in fp32
+    const int quarter = warp % 4;
+    const StateLane<D1, D2> l(quarter, lane);
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    float* dst = w.rec + ((long long)(f.rec + f.seg) * p.H + h) * (D1 * D2);
+    const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll 1
-    for (int c = (warp >> 2) - 1; c < n_chunks; c += kGroups) {
+    for (int c = 0; c < n_chunks; ++c) {
+      if (!wait(sh.sum_done + (c & 1), (c >> 1) & 1)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int at = 0; at < D2; at += 8) {
+        uint32_t r[8], u[8];
+        tmem_ld8(lane_base + C::colSumU + (c & 1) * D2 + at, u);
+        tmem_ld8(lane_base + C::colSumS + at, r);
+        tmem_wait_ld();
+        if (c > 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(__uint_as_float(r[e]) + __uint_as_float(u[e]));
+        }
+        if (c + 1 < n_chunks)
+          tmem_st8(lane_base + C::colSumS + at, u);
+        else if (at >= l.own0 && at < l.own1)
+          store_8(dst + l.row * D2 + at, u, wide);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(sh.sum_free + (c & 1));
+    }
+  } else if (warp >= 4) {
+    // two groups of eight warps, a chunk each, half a row a thread
+    const int j = (warp & 3) * 32 + lane, half = warp >> 2 & 1;
+    static_assert(kStages % 2 == 0, "a stage always falls to the same group, so that no wait is ever a phase ahead");
+#pragma unroll 1
+    for (int c = warp >= 12 ? 1 : 0; c < n_chunks; c += 2) {
       const int st = c % kStages, t = f.t0 + c * kChunk, n = min(kChunk, f.t1 - t);
-      const uint32_t tA = smem_u32(smem + C::offStage) + st * C::kStage;
+      const uint32_t sB = sStage + st * C::kSumStage;
       const float fac =
           j < n ? w.s_key * expf(g * (float)(w.reverse ? t + j + 1 - f.t0 : f.t1 - 1 - t - j)) : 0.f;
-      if (!wait(full + st, (c / kStages) & 1)) break;
       const KeyFactor kf(fac);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        uint32_t hi[D1 / 4], lo[D1 / 4];
-        if (j >= n) {
-          clear_half<D1>(tA + C::kA, j, half);
-          clear_half<D2>(tA + 2 * C::kA, j, half);
-        }
-        split_half<D1>(tA + C::kA, j, half, kf, hi, lo);
-        write_half<D1>(tA + C::kA, j, half, hi);
-        write_half<D1>(tA, j, half, lo);
+      uint32_t x[D1 / 4], rest[D1 / 4];
+      if (!wait(full + st, (c / kStages) & 1)) break;
+      if (j >= n) {
+        clear_half<D1>(sB, j, half);
+        clear_half<D2>(sB + C::kA, j, half);
       }
+      read_half<D1>(sB, j, half, x);
+      write_half<D1>(sB, j, half, x, [&](uint32_t k) { return kf.high(k); });
+      compute_again(x);
+#pragma unroll
+      for (int e = 0; e < D1 / 4; ++e) rest[e] = kf.rest(x[e]);
+      compute_again(x);
+      if (c > 0 && !wait(lo_free + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
+      write_half<D1>(sLo, j, half, x, [&](uint32_t k) { return kf.low(k); });
+      write_half<D1>(sRest, j, half, rest, [](uint32_t r) { return r; });
       fence_proxy_async_smem();
       mbar_arrive(scaled + st);
-    }
-  }
-  if (warp < 4) {
-    if (wait(mma_done, 0)) {
-      tc_fence_after();
-      write_state(tmem + ((uint32_t)(warp * 32) << 16) + C::colS, StateLane<D1, D2>(warp, lane),
-                  w.rec + ((long long)(f.rec + f.seg) * p.H + h) * (D1 * D2));
     }
   }
 }
@@ -838,12 +937,14 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
         mbar_init(sh.late + s, 1);
         mbar_init(sh.staged + s, 256);
         mbar_init(sh.done + s, 1);
-        mbar_init(sh.scaled + s, 128);
+        mbar_init(sh.scaled + s, 256);
       }
-      for (uint64_t* b : {&sh.p_full, &sh.a_done, &sh.o_full, &sh.s_done, &sh.mma_done}) mbar_init(b, 1);
-      for (uint64_t* b : {&sh.s_copied, &sh.s_scaled}) mbar_init(b, 128);
+      for (uint64_t* b : {&sh.p_full, &sh.a_done, &sh.rest_done, &sh.o_full, &sh.u_done, &sh.mma_done, sh.lo_free,
+                          sh.lo_free + 1, sh.sum_done, sh.sum_done + 1})
+        mbar_init(b, 1);
+      for (uint64_t* b : {&sh.s_copied, &sh.e_ready, sh.sum_free, sh.sum_free + 1}) mbar_init(b, 128);
       mbar_init(&sh.s_init, 512);
-      for (uint64_t* b : {&sh.w_full, &sh.hi_full, &sh.lo_full, &sh.o_free}) mbar_init(b, 256);
+      for (uint64_t* b : {&sh.w_full, &sh.hi_full, &sh.lo_full, &sh.rest_full, &sh.o_free}) mbar_init(b, 256);
       sh.abort = 0;
       fence_barrier_init();
       fence_proxy_async_smem();
@@ -854,11 +955,16 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
       prefetch_tmap(&w.b);
       prefetch_tmap(&w.c);
       prefetch_tmap(&w.o);
+      // in double: the state is multiplied by it once a chunk, for as long as it remembers
+      const double keep = exp((double)g * kChunk);
+      sh.keep[0] = (float)keep;
+      sh.keep[1] = (float)(keep - (double)sh.keep[0]);
+      sh.keep_segment = (float)exp((double)g * p.L);
     }
   } else if constexpr (!kSum) {
     for (int x = threadIdx.x - 128; x < 2 * kWeights; x += kThreads - 128) {
       const int y = first_weight(w.reverse) + x % kWeights + x / kWeights;
-      sh.weight[x] = (w.reverse ? y >= 0 : y <= 0) ? expf(g * fabsf((float)y)) : 0.f;
+      sh.weight[x] = (w.reverse ? y >= 0 : y <= 0) ? w.s_intra * expf(g * fabsf((float)y)) : 0.f;
     }
   }
   tc_fence_before();
@@ -944,9 +1050,11 @@ __global__ void __launch_bounds__(kScanThreads) decay_scan_kernel(const __grid_c
     const int seg = rev ? f.n_seg - 1 - s : s;
     return reinterpret_cast<float4*>(w.rec) + ((long long)(f.rec + seg) * p.H + h) * size4 + x;
   };
+  const float full = (float)exp((double)g * p.L);
   auto factor = [&](int s) {
     const int seg = rev ? f.n_seg - 1 - s : s;
-    return expf(g * (float)(min(p.L, f.s1 - f.s0 - seg * p.L)));
+    const int tokens = min(p.L, f.s1 - f.s0 - seg * p.L);
+    return tokens == p.L ? full : expf(g * (float)tokens);
   };
   for (int s0 = 0; s0 < f.n_seg; s0 += kAhead) {
     float4 sum[kAhead];
