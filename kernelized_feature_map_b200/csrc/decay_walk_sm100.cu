@@ -59,7 +59,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 704, kSumThreads = 768;
+constexpr int kThreads = 832, kSumThreads = 768;
 constexpr int kMaxWalks = 3;
 constexpr uint32_t kTmemCols = 512;
 
@@ -120,13 +120,13 @@ struct Shared {
   uint64_t p_full;              // P in TMEM
   uint64_t w_full;              // W written (256)
   uint64_t s_init;              // the state that enters in TMEM (512)
-  uint64_t s_copied;            // S copied to shared memory (128)
+  uint64_t s_copied;            // S copied to shared memory (256)
   uint64_t a_done;              // A has met B and S: its tile takes lo, and A S can be scaled
-  uint64_t e_ready;             // A S scaled (128)
-  uint64_t hi_full;             // hi written, rows past the end cleared (256)
+  uint64_t e_ready;             // A S scaled (256)
+  uint64_t hi_full;             // hi, or rest before it, written, rows past the end cleared (256)
   uint64_t lo_full;             // lo written (256)
-  uint64_t rest_full;           // rest written (256)
   uint64_t rest_done;           // rest has met C: its tile takes hi
+  uint64_t last_full;           // hi written after rest (256)
   uint64_t o_full;              // out complete
   uint64_t o_free;              // and read (256)
   uint64_t u_done;              // the chunk's sum complete
@@ -338,6 +338,10 @@ __device__ __forceinline__ int last_walked(const WalkParams& w, const Found& f) 
   return w.reverse ? 0 : f.n_seg - 1;
 }
 
+// Whether a state still holds a 16th or more of what entered it `tokens` ago.  If
+// not, what rest would add to it is below 2^-21 of it, and hi and lo do.
+__device__ __forceinline__ bool remembered(float g, int tokens) { return g * (float)tokens >= -2.7725887f; }
+
 // y of the first weight
 __device__ __forceinline__ int first_weight(bool reverse) { return reverse ? -32 : -128; }
 
@@ -348,9 +352,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   uint64_t *full = sh.full, *late = sh.late, *staged = sh.staged, *done = sh.done;
   uint64_t *s_init = &sh.s_init, *p_full = &sh.p_full, *w_full = &sh.w_full, *s_copied = &sh.s_copied, *e_ready = &sh.e_ready;
   uint64_t *a_done = &sh.a_done, *hi_full = &sh.hi_full, *rest_done = &sh.rest_done, *lo_full = &sh.lo_full;
-  uint64_t *rest_full = &sh.rest_full, *o_full = &sh.o_full;
+  uint64_t *last_full = &sh.last_full, *o_full = &sh.o_full;
   uint64_t *o_free = &sh.o_free, *u_done = &sh.u_done, *mma_done = &sh.mma_done;
-  const bool precise = w.fin != nullptr;  // rest reaches the state only: out is rounded to 2^-9
   const uint32_t weight = smem_u32(sh.weight);
   const uint32_t tmem = sh.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -359,6 +362,9 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   // c-th chunk walked: its first token and its tokens
   auto chunk_t = [&](int c) { return f.t0 + (rev ? n_chunks - 1 - c : c) * kChunk; };
   auto chunk_n = [&](int c) { return min(kChunk, f.t1 - chunk_t(c)); };
+  // chunks whose keys enter with their rest: those that the state which leaves remembers
+  const bool leaves = w.fin && f.row >= 0 && f.seg == last_walked(w, f);
+  auto precise = [&](int c) { return leaves && remembered(g, rev ? chunk_t(c) - f.s0 : f.s1 - chunk_t(c) - kChunk); };
   // tiles of a chunk (one thread): A and B as soon as the chunk before it in the
   // stage has been multiplied, C once that chunk's out, which leaves through its
   // C tile, has left
@@ -389,9 +395,9 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
   // starts from its scanned record, or sums those before it by itself, from the
   // copy of what enters the sequence (which the last one may be overwriting).
   constexpr int size = D1 * D2;
-  if (warp >= 4 && warp < 20 && n_chunks > 0) {
+  if (warp >= 8 && warp < 24 && n_chunks > 0) {
     constexpr int kCols = D2 / 4;
-    const int m = warp % 4 * 32 + lane, row = m % D1, at = (warp / 4 - 1) * kCols;
+    const int m = warp % 4 * 32 + lane, row = m % D1, at = (warp / 4 - 2) * kCols;
     const float* src = nullptr;
     if (split)
       src = w.rec + ((long long)(f.rec + (p.folded ? last_walked(w, f) : f.seg)) * p.H + h) * size;
@@ -444,10 +450,12 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
     mbar_arrive(s_init);
   }
 
-  if (warp < 4) {
+  if (warp < 8) {
     // --------------------------------------------------------------- S
-    const int quarter = warp;
+    const int quarter = warp % 4;
     const StateLane<D1, D2> l(quarter, lane);
+    // half of the lane's columns
+    const int c0 = l.own0 + warp / 4 * ((l.own1 - l.own0) / 2), c1 = c0 + (l.own1 - l.own0) / 2;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colS;
     const uint32_t copy = smem_u32(smem + C::offCopy);
     float* dst = w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1)
@@ -489,7 +497,6 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
           }
           if (!last) tmem_st8(lane_base + at, r[i]);
         }
-        if (at < l.own0 || at >= l.own1) return;
         if (last) {
           store_8(dst + l.row * D2 + at, r[i], wide);
         } else {
@@ -500,14 +507,14 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
           sts128(copy + unit_offset(D1, l.row, at / 8), z[0], z[1], z[2], z[3]);
         }
       };
-      fetch(0, 0);
+      fetch(c0, 0);
 #pragma unroll 1
-      for (int at = 0; at < D2; at += 16) {
+      for (int at = c0; at < c1; at += 16) {
         tmem_wait_ld();
         fetch(at + 8, 1);
         step(at, 0);
         tmem_wait_ld();
-        if (at + 16 < D2) fetch(at + 16, 0);
+        if (at + 16 < c1) fetch(at + 16, 0);
         step(at + 8, 1);
       }
       if (last) break;
@@ -520,20 +527,20 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       const float reach = w.s_inter * power(rev ? max(n - 1 - i, 0) : i + 1);
       if (!wait(a_done, c & 1)) break;
       tc_fence_after();
-      scale_columns<D2>(lane_base - C::colS + C::colE, reach);
+      scale_columns<D2 / 2>(lane_base - C::colS + C::colE + warp / 4 * (D2 / 2), reach);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(e_ready);
     }
     if (n_chunks == 0 && dst) {  // an empty sequence leaves what it starts from
       const float* src = w.init && f.resumed ? w.init + ((long long)f.row * p.H + h) * size : nullptr;
-      for (int j = l.own0; j < l.own1; ++j)
+      for (int j = c0; j < c1; ++j)
         dst[l.row * D2 + j] = src ? src[w.init_transposed ? j * D1 + l.row : l.row * D2 + j] : 0.f;
     }
     griddep_wait();  // a grid ends after those it was launched behind
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // --------------------------------------------------------------- W and out
-    const int quarter = warp % 4, half = warp >= 8 ? 1 : 0;
+    const int quarter = warp % 4, half = warp >= 12 ? 1 : 0;
     const int i = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     // Of the four blocks of 32 columns of a row, one warp takes the outer two and
@@ -607,7 +614,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       if (n == kChunk) fence_proxy_async_smem();
       mbar_arrive(staged + c % kStages);
     }
-  } else if (warp == 21) {
+  } else if (warp == 25) {
     // --------------------------------------------------------------- copies: tiles in, out
     int loaded = min(kStages, n_chunks), loaded_late = loaded;
     if (lane == 0) {
@@ -648,13 +655,14 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
 #pragma unroll 1
     for (int c = max(loaded_late - kStages, 0); c < loaded_late; ++c)
       mbar_wait_drain(late + c % kStages, (c / kStages) & 1);
-  } else if (warp == 20) {
+  } else if (warp == 24) {
     // --------------------------------------------------------------- MMA
     constexpr uint32_t id_p = idesc_bf16(128, 128, false, false);  // A, B both K-major
     constexpr uint32_t id_o = idesc_bf16(128, D2, false, true);    // A or W, and C or the copy of S (N-major)
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);     // B^T (M-major), C (N-major)
     const uint32_t sStage = smem_u32(smem + C::offStage);
     const uint64_t dcopy = smem_desc(smem_u32(smem + C::offCopy), D1 * 128, 1024, kSw128);
+    int rests = 0;
 #pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
@@ -696,19 +704,21 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
         mma_commit(a_done);
       }
       __syncwarp();
-      // smallest first: what the accumulation truncates is a part of what is there
+      // rest, lo, hi: what the accumulation truncates is a part of what is there; hi, lo without a rest
+      const bool all = precise(c);
       if (!wait(late + st, (c / kStages) & 1)) break;
-      if (precise) {
-        if (!wait(rest_full, c & 1)) break;
-        tc_fence_after();
-        add_keys(kB, true, rest_done);
-      }
-      if (!wait(lo_full, c & 1)) break;
-      tc_fence_after();
-      add_keys(kA, !precise, nullptr);
       if (!wait(hi_full, c & 1)) break;
       tc_fence_after();
-      add_keys(kB, false, u_done);
+      add_keys(kB, true, all ? rest_done : nullptr);
+      if (!wait(lo_full, c & 1)) break;
+      tc_fence_after();
+      add_keys(kA, false, all ? nullptr : u_done);
+      if (all) {
+        if (!wait(last_full, rests & 1)) break;
+        tc_fence_after();
+        add_keys(kB, false, u_done);
+        ++rests;
+      }
       if (!wait(w_full, c & 1)) break;
       if (!wait(e_ready, c & 1)) break;
       tc_fence_after();
@@ -726,7 +736,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
     mbar_wait_drain(mma_done, 0);
   } else {
     // --------------------------------------------------------------- B
-    const int j = (warp & 3) * 32 + lane, half = warp >= 16 ? 1 : 0;  // token of the chunk, half of its row
+    const int j = (warp & 3) * 32 + lane, half = warp >= 20 ? 1 : 0;  // token of the chunk, half of its row
+    int rests = 0;
 #pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages, n = chunk_n(c);
@@ -742,21 +753,26 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       }
       read_half<D1>(tA + C::kA, j, half, x);
       if (!wait(p_full, c & 1)) break;
-      if (precise) {
+      const bool all = precise(c);
+      if (all)
         write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.rest(k); });
-        fence_proxy_async_smem();
-        mbar_arrive(rest_full);
-        compute_again(x);
-      }
+      else
+        write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.high(k); });
+      fence_proxy_async_smem();
+      mbar_arrive(hi_full);
+      compute_again(x);
       if (!wait(a_done, c & 1)) break;
       write_half<D1>(tA, j, half, x, [&](uint32_t k) { return kf.low(k); });
       fence_proxy_async_smem();
       mbar_arrive(lo_full);
-      compute_again(x);
-      if (precise && !wait(rest_done, c & 1)) break;
-      write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.high(k); });
-      fence_proxy_async_smem();
-      mbar_arrive(hi_full);
+      if (all) {
+        compute_again(x);
+        if (!wait(rest_done, rests & 1)) break;
+        write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.high(k); });
+        fence_proxy_async_smem();
+        mbar_arrive(last_full);
+        ++rests;
+      }
     }
   }
 }
@@ -777,6 +793,10 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
   const uint32_t sStage = smem_u32(smem), sLo = sStage + C::offLo, sRest = sLo + C::kA;
+  auto precise = [&](int c) {
+    const int t = f.t0 + c * kChunk;
+    return w.fin && remembered(g, w.reverse ? t - f.s0 : f.s1 - t - kChunk);
+  };
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, &sh.abort, bar, parity); };
   if (warp == 0) {
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);
@@ -792,13 +812,13 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
       tc_fence_after();
       // smallest first, into an accumulator of the chunk's own
 #pragma unroll 1
-      for (int part = 0; part < 3; ++part) {
+      for (int part = precise(c) ? 0 : 1; part < 3; ++part) {
         const uint64_t dK = key_desc<D1>(part == 0 ? sRest : part == 1 ? sLo : sB);
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < kChunk / 16; ++ks)
             mma_ss(tmem + C::colSumU + (c & 1) * D2, desc_add(dK, ks * 2048), desc_add(dC, ks * 2048), id_s,
-                   part + ks > 0);
+                   part > (precise(c) ? 0 : 1) || ks > 0);
         }
         __syncwarp();
       }
@@ -867,7 +887,7 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
       const float fac =
           j < n ? w.s_key * expf(g * (float)(w.reverse ? t + j + 1 - f.t0 : f.t1 - 1 - t - j)) : 0.f;
       const KeyFactor kf(fac);
-      uint32_t x[D1 / 4], rest[D1 / 4];
+      uint32_t x[D1 / 4], lo[D1 / 4];
       if (!wait(full + st, (c / kStages) & 1)) break;
       if (j >= n) {
         clear_half<D1>(sB, j, half);
@@ -877,11 +897,16 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
       write_half<D1>(sB, j, half, x, [&](uint32_t k) { return kf.high(k); });
       compute_again(x);
 #pragma unroll
-      for (int e = 0; e < D1 / 4; ++e) rest[e] = kf.rest(x[e]);
+      for (int e = 0; e < D1 / 4; ++e) lo[e] = kf.low(x[e]);
       compute_again(x);
+      const bool all = precise(c);
+      if (all) {
+#pragma unroll
+        for (int e = 0; e < D1 / 4; ++e) x[e] = kf.rest(x[e]);
+      }
       if (c > 0 && !wait(lo_free + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
-      write_half<D1>(sLo, j, half, x, [&](uint32_t k) { return kf.low(k); });
-      write_half<D1>(sRest, j, half, rest, [](uint32_t r) { return r; });
+      write_half<D1>(sLo, j, half, lo, [](uint32_t r) { return r; });
+      if (all) write_half<D1>(sRest, j, half, x, [](uint32_t r) { return r; });
       fence_proxy_async_smem();
       mbar_arrive(scaled + st);
     }
@@ -942,9 +967,9 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
       for (uint64_t* b : {&sh.p_full, &sh.a_done, &sh.rest_done, &sh.o_full, &sh.u_done, &sh.mma_done, sh.lo_free,
                           sh.lo_free + 1, sh.sum_done, sh.sum_done + 1})
         mbar_init(b, 1);
-      for (uint64_t* b : {&sh.s_copied, &sh.e_ready, sh.sum_free, sh.sum_free + 1}) mbar_init(b, 128);
+      for (uint64_t* b : {sh.sum_free, sh.sum_free + 1}) mbar_init(b, 128);
       mbar_init(&sh.s_init, 512);
-      for (uint64_t* b : {&sh.w_full, &sh.hi_full, &sh.lo_full, &sh.rest_full, &sh.o_free}) mbar_init(b, 256);
+      for (uint64_t* b : {&sh.s_copied, &sh.e_ready, &sh.w_full, &sh.hi_full, &sh.lo_full, &sh.last_full, &sh.o_free}) mbar_init(b, 256);
       sh.abort = 0;
       fence_barrier_init();
       fence_proxy_async_smem();
