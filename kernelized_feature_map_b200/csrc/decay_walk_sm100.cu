@@ -225,7 +225,7 @@ __device__ __forceinline__ void store_32b(void* to, const uint32_t* z) {
 }
 
 // 8 values, a whole sector where they start on one
-__device__ __forceinline__ void store_8(float* to, const uint32_t (&x)[8], bool wide) {
+__device__ __forceinline__ void store_8(float* to, const uint32_t* x, bool wide) {
   if (wide) {
     store_32b(to, x);
   } else {
@@ -467,8 +467,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
     for (int c = 0; ok && c <= n_chunks && n_chunks > 0; ++c) {
       // The state before chunk c (c = n_chunks: the one that leaves): a^n S + U of
       // the chunk before, added in fp32 (the tensor core's accumulation truncates:
-      // onto S it would cost 6e-7 of it every chunk).  8 columns at a time, and the
-      // next 8 on their way.
+      // onto S it would cost 6e-7 of it every chunk).  16 columns at a time.
       float k0 = 1.f, k1 = 0.f;
       const bool add = c > 0, last = c == n_chunks;
       if (add) {
@@ -481,41 +480,35 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       tc_fence_after();
       const uint64_t keep = f32x2(__float_as_uint(k0), __float_as_uint(k0));
       const uint64_t more = f32x2(__float_as_uint(k1), __float_as_uint(k1));
-      uint32_t r[2][8], u[2][8];
-      auto fetch = [&](int at, int i) {
-        tmem_ld8(lane_base + at, r[i]);
-        tmem_ld8(lane_base - C::colS + C::colU + at, u[i]);  // before the first chunk: not used
-      };
-      auto step = [&](int at, int i) {
-        if (add) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t x = f32x2(r[i][2 * k], r[i][2 * k + 1]);
-            const uint64_t v = f32x2_fma(x, keep, f32x2_fma(x, more, f32x2(u[i][2 * k], u[i][2 * k + 1])));
-            r[i][2 * k] = (uint32_t)v;
-            r[i][2 * k + 1] = (uint32_t)(v >> 32);
-          }
-          if (!last) tmem_st8(lane_base + at, r[i]);
-        }
-        if (last) {
-          store_8(dst + l.row * D2 + at, r[i], wide);
-        } else {
-          uint32_t z[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            z[k] = pack_bf16x2(__uint_as_float(r[i][2 * k]), __uint_as_float(r[i][2 * k + 1]));
-          sts128(copy + unit_offset(D1, l.row, at / 8), z[0], z[1], z[2], z[3]);
-        }
-      };
-      fetch(c0, 0);
 #pragma unroll 1
       for (int at = c0; at < c1; at += 16) {
+        uint32_t r[16], u[16];
+        tmem_ld16(lane_base + at, r);
+        tmem_ld16(lane_base - C::colS + C::colU + at, u);  // before the first chunk: not used
         tmem_wait_ld();
-        fetch(at + 8, 1);
-        step(at, 0);
-        tmem_wait_ld();
-        if (at + 16 < c1) fetch(at + 16, 0);
-        step(at + 8, 1);
+        if (add) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t x = f32x2(r[2 * k], r[2 * k + 1]);
+            const uint64_t v = f32x2_fma(x, keep, f32x2_fma(x, more, f32x2(u[2 * k], u[2 * k + 1])));
+            r[2 * k] = (uint32_t)v;
+            r[2 * k + 1] = (uint32_t)(v >> 32);
+          }
+          if (!last) tmem_st16(lane_base + at, r);
+        }
+        if (last) {
+          store_8(dst + l.row * D2 + at, r, wide);
+          store_8(dst + l.row * D2 + at + 8, r + 8, wide);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
+            sts128(copy + unit_offset(D1, l.row, at / 8 + e), z[0], z[1], z[2], z[3]);
+          }
+        }
       }
       if (last) break;
       tmem_wait_st();
