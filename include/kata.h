@@ -474,9 +474,12 @@ kata_status_t kata_decode_step_sg(const void* q, const void* k, const void* v, v
  * sequence of the call names too, records KATA_ERR_INVALID_ARG and counts
  * as negative.  A sequence of length 0 leaves the state it starts from.
  * bf16; d and dv in {64, 128}; others KATA_ERR_UNSUPPORTED.  Tensor-core
- * arithmetic with fp32 accumulation; the state is carried in fp32, k scaled
- * by its decay enters it as a sum of two bf16 values, and a bf16 copy of it
- * is multiplied by q.
+ * arithmetic with fp32 accumulation: the state is carried in fp32, k scaled
+ * by its decay enters it as a sum of bf16 values (three where the state that
+ * leaves still holds a 16th or more of what enters, otherwise two), and a bf16
+ * copy of the state is multiplied by q.  Infinities and NaN in a sequence's
+ * tokens may reach all rows of their 128 tokens' chunk and the chunks after;
+ * no other sequence's.  o must not overlap q, k or v.
  * workspace: kata_fwd_linear_decay_workspace_size() bytes (0 for short
  * calls: NULL allowed), 256-byte aligned.  Repeated calls give bitwise the
  * same result.
@@ -518,7 +521,8 @@ kata_status_t kata_bwd_linear_decay(const void* q, const void* k, const void* v,
  * its row of o is written as zeros and no state is touched.  A slot of
  * n_slots or more, or one that an earlier stream of the call names too,
  * counts as negative and records KATA_ERR_INVALID_ARG in the status word.
- * d and dv in {64, 128}; fp32 arithmetic throughout.
+ * d and dv in {64, 128}; fp32 arithmetic throughout.  o must not overlap q, k
+ * or v.
  */
 kata_status_t kata_decode_step_linear_decay(const void* q, const void* k, const void* v, void* o, float* S,
                                             int n, int H, int d, int dv,

@@ -3,7 +3,7 @@
 //
 // These calls are made once per layer and token, where the arithmetic takes a
 // few microseconds; a binding through ctypes, with its checks in Python, takes
-// 17 to 24 us for one of them, this one 4 to 6.
+// 17 to 24 us for one of them, this one 3 to 4.5.
 //
 // Token tensors are [T, H, width] with the last two dimensions dense; the
 // stride between tokens is free (a multiple of 16 bytes), so the parts of a

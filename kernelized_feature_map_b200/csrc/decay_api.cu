@@ -171,7 +171,7 @@ static kata_status_t check_q8(const void* S, const void* z, const void* cache, c
                               int dv) {
   if (n < 0 || n_slots < 0 || n_entries < 0 || H < 1 || rows < 1) return KATA_ERR_INVALID_ARG;
   if (dv != 16 && dv != 64 && dv != 128) return KATA_ERR_UNSUPPORTED;
-  // one grid row per pair, and 32-row tiles of the H * rows rows along the other axis
+  // one grid row per pair, and tiles of 64 or more of the H * rows rows along the other axis
   if (n > 65535 || (long long)H * rows > (1ll << 30)) return KATA_ERR_UNSUPPORTED;
   if ((z == nullptr) != (z_cache == nullptr)) return KATA_ERR_INVALID_ARG;
   if ((!slots && n > n_slots) || (!entries && n > n_entries)) return KATA_ERR_INVALID_ARG;

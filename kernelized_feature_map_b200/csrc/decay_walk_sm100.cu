@@ -8,42 +8,58 @@
 //   P     = A B^T                              [128 x 128]
 //   W_ij  = a^(i-j) P_ij for j <= i, else 0    rounded to bf16
 //   out_i = scale (sum_j W_ij C_j + a^(i+1) A_i S)
-//   S     = a^r S + sum_j (a^(r-1-j) B_j) C_j^T
+//   U     = sum_j (a^(r-1-j) B_j) C_j^T,   S <- a^r S + U
 // and backwards, where the entering state already belongs to the chunk's last
 // token: W_ij = a^(j-i) P_ij for j >= i, the reach of S is a^(r-1-i) and B_j
 // enters with a^(j+1), times the scale (S is then the gradient itself, which
 // the entering gradient joins unscaled).
 //
-// Roundings.  S is fp32, in TMEM for the whole walk: the tensor cores
-// accumulate onto it.  The scaled B_j would lose 2^-9 of the state if it went
-// in as one bf16; it goes in as two, hi + lo (error 2^-17, the state agrees
-// with fp32 arithmetic), at the price of a second pass of that product.  W
-// and the copy of S that A is multiplied with are rounded to bf16 once: they
-// reach only out, which is rounded as far itself.
+// Roundings.  S is fp32, in TMEM for the whole walk.  The tensor cores truncate
+// as they accumulate, so U is summed for itself, smallest part first, and added
+// to S by the CUDA cores; a^128 is held as the sum of two fp32 values.  A scaled
+// key enters U as two bf16 values (it loses 2^-17), as three (2^-25) where the
+// chunk is still an 1/16 or more of the state that leaves: that state then
+// agrees with fp32 arithmetic (1e-7 to 3e-7 of it in the mean square).  W and
+// the copy of S that A is multiplied with are rounded to bf16 once: they reach
+// only out, which is rounded as far itself.
 //
 // One CTA per segment of a sequence, head and walk (1 CTA per SM: 512 TMEM
-// columns).  Warps (640 threads):
-//   0       TMA: A, B, C tiles of the chunks into a ring of kStages
-//   1       TMEM allocator; MMA issue (whole warp, one elected lane)
-//   4-7     W from P, a TMEM lane quarter each (as the next two roles)
-//   8-11    out from the two accumulators
-//   12-15   S: the bf16 copy for the next chunk, and its scaling in TMEM
-//   16-19   B: hi in place over the tile once P is done, lo over the A tile once
-//           A has met S; rows past the sequence's end cleared in B and C,
-//           so that nothing of the next sequence (NaN included) gets in
-// MMA order per chunk: P; A S; hi; W C; lo.  The state of the next chunk
-// waits only for lo, and while it is copied and scaled P and W of the next
-// chunk proceed.
+// columns, 26 warps of 72 registers):
+//   0-7    S: a^r S + U, its bf16 copy for A S, and A S times the reach; the state
+//          that leaves
+//   8-15   W from P, over it; then out, through the chunk's C tile
+//   16-23  keys: rest or hi in place over B once P is done, lo over A once A has
+//          met S; rows past the sequence's end cleared in B and C, so that nothing
+//          of the next sequence (NaN included) gets in
+//   24     MMA issue (whole warp, one elected lane)
+//   25     TMA: A, B, C tiles in, out
+// Warps 8-23 also bring the state that enters.  A role has at least one warp per
+// TMEM lane quarter.  MMA order per chunk: P; A S; the keys' parts; W C onto A S.
+// An A and a B tile are loaded again once every product of the chunk is done, a C
+// tile once out, written over it, has left.
 //
-// TMEM columns: P (W over it) 128 | W C d2 | A S d2 | S d2.  With d1 = 64 the
+// TMEM columns: P (W over it) 128 | A S, W C d2 | U d2 | S d2.  With d1 = 64 the
 // state product still has 128 rows: its A operand reads the 64 columns twice
 // (leading offset 0), so lanes 64-127 hold a second copy of S, and the two
 // halves of the warps write one half of the bf16 copy each.
 //
-// Long sequences with few heads do not fill the SMs: they are cut into
-// segments of L tokens.  decay_walk_kernel<.., true> first sums each segment
-// from a zero state, decay_scan_kernel turns the sums into the states entering
-// the segments, and the walks start from those (kata_internal.h, plan below).
+// Long sequences with few heads do not fill the SMs: they are cut into segments
+// of L tokens.  decay_walk_kernel<.., true> first sums each segment from a zero
+// state (the one walked last excepted); a walk then starts from the sums before
+// its segment, which it adds up itself, or for 16 segments and more
+// decay_scan_kernel does (plan below).
+//
+// What bounds it.  A chunk's critical path is work of CUDA cores on tiles (S and
+// its copy, then keys and W side by side, then A S, then out) with four short
+// products between: 6200 cycles a chunk at d = dv = 128, of which the tensor pipe
+// works 37%; its tiles cross shared memory in 4700 cycles, and at 148 SMs its
+// bytes HBM in 5500.  Measured: 131072 tokens, 16 heads, d = dv = 128 765 us, 2.8
+// TB/s of q, k, v and o; 220 us of it are the segments' sums, which read k and v
+// once more.  8192 tokens in 13 sequences: 85 us.  75 tokens, d = dv = 64: 8.3 us,
+// a launch and one chunk's path.  Gradients, 8 x 2048 tokens, 16 heads, d = dv =
+// 128: 205 us.  Tried and not faster: fewer warps with more registers each, out by
+// warps of its own, two accumulators for out, A S ahead of P, W in blocks of 32
+// columns (spills), lo in place ahead of A S (spills, prompts 10% slower).
 #include <cuda.h>
 
 #include <algorithm>
@@ -1048,7 +1064,10 @@ __global__ void __launch_bounds__(kScanThreads) decay_scan_kernel(const __grid_c
   }
   __syncthreads();
   const Found f = found;
-  if (f.seq < 0) return;
+  if (f.seq < 0) {
+    griddep_wait();  // a grid ends after those it was launched behind
+    return;
+  }
   const bool rev = w.reverse != 0;
   const int d1 = w.swapped ? d_b : d_a, d2 = w.swapped ? d_a : d_b;
   const int size4 = d1 * d2 / 4, x = blockIdx.x % part * kScanThreads + threadIdx.x;
