@@ -110,12 +110,12 @@ struct Cfg {
   static constexpr int kStages = kFit > 4 ? 4 : kFit;                // 2 (128, 128) .. 4 (64, 64)
   static constexpr int offStage = 0;
   static constexpr int offCopy = kStages * kStage;
-  // the sum: stages [B | C], then lo and rest
+  // the sum: stages [B | C], then lo
   static constexpr int kSumStage = kA + kC;
-  static constexpr int kSumStages = (224 * 1024 - 2 * kA) / kSumStage >= 4 ? 4 : 2;
+  static constexpr int kSumStages = (224 * 1024 - kA) / kSumStage >= 4 ? 4 : 3;  // 3 (128, 128), else 4
   static constexpr int offLo = kSumStages * kSumStage;
   static constexpr int kBytes =
-      (offCopy + kCopy > offLo + 2 * kA ? offCopy + kCopy : offLo + 2 * kA) + 1024;  // + alignment slack
+      (offCopy + kCopy > offLo + kA ? offCopy + kCopy : offLo + kA) + 1024;  // + alignment slack
   static constexpr uint32_t colP = 0, colE = 128, colU = 128 + D2, colS = 128 + 2 * D2;
   static constexpr uint32_t colSumU = 0, colSumS = 2 * D2;  // the sum: two accumulators, and the sum
 };
@@ -132,7 +132,7 @@ struct Shared {
   uint64_t staged[kMaxStages];  // out in shared memory (256)
   uint64_t done[kMaxStages];    // every product of the chunk complete
   uint64_t scaled[kMaxStages];  // the sum's scaled keys written (256)
-  uint64_t lo_free[2];          // the sum's lo and rest read, of even and odd chunks
+  uint64_t lo_free[2];          // the sum's lo read, of even and odd chunks
   uint64_t p_full;              // P in TMEM
   uint64_t w_full;              // W written (256)
   uint64_t s_init;              // the state that enters in TMEM (512)
@@ -141,8 +141,8 @@ struct Shared {
   uint64_t e_ready;             // A S scaled (256)
   uint64_t hi_full;             // hi, or rest before it, written, rows past the end cleared (256)
   uint64_t lo_full;             // lo written (256)
-  uint64_t rest_done;           // rest has met C: its tile takes hi
-  uint64_t last_full;           // hi written after rest (256)
+  uint64_t rest_done;           // rest has met C: its tile takes hi (the sum: lo)
+  uint64_t last_full;           // hi (the sum: lo) written after rest (256)
   uint64_t o_full;              // out complete
   uint64_t o_free;              // and read (256)
   uint64_t u_done;              // the chunk's sum complete
@@ -801,7 +801,7 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
   const uint32_t tmem = sh.tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_chunks = (f.t1 - f.t0 + kChunk - 1) / kChunk;
-  const uint32_t sStage = smem_u32(smem), sLo = sStage + C::offLo, sRest = sLo + C::kA;
+  const uint32_t sStage = smem_u32(smem), sLo = sStage + C::offLo;
   auto precise = [&](int c) {
     const int t = f.t0 + c * kChunk;
     return w.fin && remembered(g, w.reverse ? t - f.s0 : f.s1 - t - kChunk);
@@ -809,6 +809,7 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_on(p.wc, &sh.abort, bar, parity); };
   if (warp == 0) {
     constexpr uint32_t id_s = idesc_bf16(128, D2, true, true);
+    int rests = 0;
 #pragma unroll 1
     for (int c = 0; c < n_chunks; ++c) {
       const int st = c % kStages;
@@ -820,17 +821,26 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
       if (c > 1 && !wait(sh.sum_free + (c & 1), ((c >> 1) - 1) & 1)) break;
       tc_fence_after();
       // smallest first, into an accumulator of the chunk's own
-#pragma unroll 1
-      for (int part = precise(c) ? 0 : 1; part < 3; ++part) {
-        const uint64_t dK = key_desc<D1>(part == 0 ? sRest : part == 1 ? sLo : sB);
+      auto add = [&](uint32_t keys, bool first) {
+        const uint64_t dK = key_desc<D1>(keys);
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < kChunk / 16; ++ks)
             mma_ss(tmem + C::colSumU + (c & 1) * D2, desc_add(dK, ks * 2048), desc_add(dC, ks * 2048), id_s,
-                   part > (precise(c) ? 0 : 1) || ks > 0);
+                   !first || ks > 0);
         }
         __syncwarp();
+      };
+      const bool all = precise(c);
+      add(sLo, true);  // rest where there is one
+      if (all) {
+        mma_commit_w(&sh.rest_done);
+        if (!wait(&sh.last_full, rests & 1)) break;
+        tc_fence_after();
+        add(sLo, false);
+        ++rests;
       }
+      add(sB, false);
       mma_commit_w(sh.sum_done + (c & 1));
       mma_commit_w(empty + st);
       mma_commit_w(lo_free + (c & 1));
@@ -888,15 +898,23 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
   } else if (warp >= 4) {
     // two groups of eight warps, a chunk each, half a row a thread
     const int j = (warp & 3) * 32 + lane, half = warp >> 2 & 1;
-    static_assert(kStages % 2 == 0, "a stage always falls to the same group, so that no wait is ever a phase ahead");
+    // No wait is a phase ahead: a group that waits for chunk c + 2 has seen the
+    // products of chunk c - 1 complete (lo_free), the last that used its stage.
+    static_assert(kStages >= 3, "stages");
+    int rests = 0;  // of the chunks before c
 #pragma unroll 1
-    for (int c = warp >= 12 ? 1 : 0; c < n_chunks; c += 2) {
+    for (int c = 0; c < n_chunks; ++c) {
+      const bool all = precise(c);
+      if ((c & 1) != (warp >= 12 ? 1 : 0)) {
+        rests += all;
+        continue;
+      }
       const int st = c % kStages, t = f.t0 + c * kChunk, n = min(kChunk, f.t1 - t);
       const uint32_t sB = sStage + st * C::kSumStage;
       const float fac =
           j < n ? w.s_key * expf(g * (float)(w.reverse ? t + j + 1 - f.t0 : f.t1 - 1 - t - j)) : 0.f;
       const KeyFactor kf(fac);
-      uint32_t x[D1 / 4], lo[D1 / 4];
+      uint32_t x[D1 / 4];
       if (!wait(full + st, (c / kStages) & 1)) break;
       if (j >= n) {
         clear_half<D1>(sB, j, half);
@@ -905,17 +923,24 @@ __device__ void sum_segment(const Params& p, const WalkParams& w, int h, float g
       read_half<D1>(sB, j, half, x);
       write_half<D1>(sB, j, half, x, [&](uint32_t k) { return kf.high(k); });
       compute_again(x);
+      if (!all) {
 #pragma unroll
-      for (int e = 0; e < D1 / 4; ++e) lo[e] = kf.low(x[e]);
-      compute_again(x);
-      const bool all = precise(c);
-      if (all) {
-#pragma unroll
-        for (int e = 0; e < D1 / 4; ++e) x[e] = kf.rest(x[e]);
+        for (int e = 0; e < D1 / 4; ++e) x[e] = kf.low(x[e]);
       }
       if (c > 0 && !wait(lo_free + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
-      write_half<D1>(sLo, j, half, lo, [](uint32_t r) { return r; });
-      if (all) write_half<D1>(sRest, j, half, x, [](uint32_t r) { return r; });
+      if (all) {
+        write_half<D1>(sLo, j, half, x, [&](uint32_t k) { return kf.rest(k); });
+        fence_proxy_async_smem();
+        mbar_arrive(scaled + st);
+        compute_again(x);
+        if (!wait(&sh.rest_done, rests & 1)) break;
+        write_half<D1>(sLo, j, half, x, [&](uint32_t k) { return kf.low(k); });
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.last_full);
+        ++rests;
+        continue;
+      }
+      write_half<D1>(sLo, j, half, x, [](uint32_t k) { return k; });
       fence_proxy_async_smem();
       mbar_arrive(scaled + st);
     }
