@@ -308,12 +308,19 @@ struct KeyFactor {
   }
 };
 
-// One half of a row of D values from its tile
+// The first unit of one half of a row of D values; unit u is at this ^ 16 u (tiles
+// are 1024-byte aligned).
+template <int D>
+__device__ __forceinline__ uint32_t half_row(uint32_t tile, int j, int half) {
+  return tile + unit_offset(kChunk, j, half * (D / 16));
+}
+// One half of a row from its tile
 template <int D>
 __device__ __forceinline__ void read_half(uint32_t tile, int j, int half, uint32_t (&x)[D / 4]) {
+  const uint32_t row = half_row<D>(tile, j, half);
 #pragma unroll
   for (int u = 0; u < D / 16; ++u) {
-    const uint4 v = lds128(tile + unit_offset(kChunk, j, half * (D / 16) + u));
+    const uint4 v = lds128(row ^ 16 * u);
     x[4 * u] = v.x;
     x[4 * u + 1] = v.y;
     x[4 * u + 2] = v.z;
@@ -330,17 +337,18 @@ __device__ __forceinline__ void compute_again(uint32_t (&x)[N]) {
 // and, through a function of each pair, to one
 template <int D, typename F>
 __device__ __forceinline__ void write_half(uint32_t tile, int j, int half, const uint32_t (&x)[D / 4], F of) {
+  const uint32_t row = half_row<D>(tile, j, half);
 #pragma unroll
   for (int u = 0; u < D / 16; ++u)
-    sts128(tile + unit_offset(kChunk, j, half * (D / 16) + u), of(x[4 * u]), of(x[4 * u + 1]), of(x[4 * u + 2]),
+    sts128(row ^ 16 * u, of(x[4 * u]), of(x[4 * u + 1]), of(x[4 * u + 2]),
            of(x[4 * u + 3]));
 }
 // a half row of zeros
 template <int D>
 __device__ __forceinline__ void clear_half(uint32_t tile, int j, int half) {
+  const uint32_t row = half_row<D>(tile, j, half);
 #pragma unroll
-  for (int u = 0; u < D / 16; ++u)
-    sts128(tile + unit_offset(kChunk, j, half * (D / 16) + u), 0u, 0u, 0u, 0u);
+  for (int u = 0; u < D / 16; ++u) sts128(row ^ 16 * u, 0u, 0u, 0u, 0u);
 }
 
 // descriptors of the state's products: scaled keys (M-major), and the C tile (N-major)
@@ -473,7 +481,8 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
     // half of the lane's columns
     const int c0 = l.own0 + warp / 4 * ((l.own1 - l.own0) / 2), c1 = c0 + (l.own1 - l.own0) / 2;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + C::colS;
-    const uint32_t copy = smem_u32(smem + C::offCopy);
+    // the lane's row of the copy: its columns are of one atom, unit u of it at copy ^ 16 u
+    const uint32_t copy = smem_u32(smem + C::offCopy) + unit_offset(D1, l.row, c0 / 64 * 8);
     float* dst = w.fin && f.row >= 0 && f.seg == (rev ? 0 : f.n_seg - 1)
                      ? w.fin + ((long long)f.row * p.H + h) * size
                      : nullptr;
@@ -522,7 +531,7 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               z[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]), __uint_as_float(r[8 * e + 2 * k + 1]));
-            sts128(copy + unit_offset(D1, l.row, at / 8 + e), z[0], z[1], z[2], z[3]);
+            sts128(copy ^ 16 * ((at / 8 + e) & 7), z[0], z[1], z[2], z[3]);
           }
         }
       }
@@ -609,10 +618,11 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
 #pragma unroll
         for (int e = 0; e < 16; ++e) z[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
         if (n == kChunk) {
-          const uint32_t stage = smem_u32(smem + C::offStage) + c % kStages * C::kStage + 2 * C::kA;
+          const uint32_t orow = smem_u32(smem + C::offStage) + c % kStages * C::kStage + 2 * C::kA +
+                                unit_offset(kChunk, i, half * (D2 / 16) & ~7);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            sts128(stage + unit_offset(kChunk, i, at / 8 + e), z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+            sts128(orow ^ 16 * ((at / 8 + e) & 7), z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
         } else if (i < n) {
           uint4* orow =
               reinterpret_cast<uint4*>(w.out + (long long)(chunk_t(c) + i) * w.out_stride + (long long)h * D2 + at);
@@ -762,25 +772,36 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       }
       read_half<D1>(tA + C::kA, j, half, x);
       if (!wait(p_full, c & 1)) break;
-      const bool all = precise(c);
-      if (all)
+      if (precise(c)) {
         write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.rest(k); });
-      else
-        write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.high(k); });
-      fence_proxy_async_smem();
-      mbar_arrive(hi_full);
-      compute_again(x);
-      if (!wait(a_done, c & 1)) break;
-      write_half<D1>(tA, j, half, x, [&](uint32_t k) { return kf.low(k); });
-      fence_proxy_async_smem();
-      mbar_arrive(lo_full);
-      if (all) {
+        fence_proxy_async_smem();
+        mbar_arrive(hi_full);
+        compute_again(x);
+        if (!wait(a_done, c & 1)) break;
+        write_half<D1>(tA, j, half, x, [&](uint32_t k) { return kf.low(k); });
+        fence_proxy_async_smem();
+        mbar_arrive(lo_full);
         compute_again(x);
         if (!wait(rest_done, rests & 1)) break;
         write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.high(k); });
         fence_proxy_async_smem();
         mbar_arrive(last_full);
         ++rests;
+      } else {
+        write_half<D1>(tA + C::kA, j, half, x, [&](uint32_t k) { return kf.high(k); });
+        fence_proxy_async_smem();
+        mbar_arrive(hi_full);
+        compute_again(x);
+        // lo, while A meets S
+#pragma unroll
+        for (int e = 0; e < D1 / 4; ++e) {
+          x[e] = kf.low(x[e]);
+          
+        }
+        if (!wait(a_done, c & 1)) break;
+        write_half<D1>(tA, j, half, x, [](uint32_t k) { return k; });
+        fence_proxy_async_smem();
+        mbar_arrive(lo_full);
       }
     }
   }
