@@ -51,15 +51,17 @@
 //
 // What bounds it.  A chunk's critical path is work of CUDA cores on tiles (S and
 // its copy, then keys and W side by side, then A S, then out) with four short
-// products between: 6200 cycles a chunk at d = dv = 128, of which the tensor pipe
-// works 37%; its tiles cross shared memory in 4700 cycles, and at 148 SMs its
-// bytes HBM in 5500.  Measured: 131072 tokens, 16 heads, d = dv = 128 765 us, 2.8
-// TB/s of q, k, v and o; 220 us of it are the segments' sums, which read k and v
-// once more.  8192 tokens in 13 sequences: 85 us.  75 tokens, d = dv = 64: 8.3 us,
-// a launch and one chunk's path.  Gradients, 8 x 2048 tokens, 16 heads, d = dv =
-// 128: 205 us.  Tried and not faster: fewer warps with more registers each, out by
-// warps of its own, two accumulators for out, A S ahead of P, W in blocks of 32
-// columns (spills), lo in place ahead of A S (spills, prompts 10% slower).
+// products between: 5500 cycles a chunk at d = dv = 128, of which the tensor pipe
+// works 38%; its tiles cross shared memory in 4700 cycles, and at 148 SMs its
+// bytes HBM in 5500.  The sums, of which no chunk waits for another, are bound by
+// the loads in flight (three stages 4.6 TB/s, two 3.7).  Measured: 131072 tokens,
+// 16 heads, d = dv = 128 670 to 710 us, 3.2 TB/s of q, k, v and o; a quarter of it
+// are the segments' sums, which read k and v once more.  8192 tokens in 13
+// sequences: 81 us.  75 tokens, d = dv = 64: 8.3 us, a launch and one chunk's path.
+// Gradients, 8 x 2048 tokens, 16 heads, d = dv = 128: 190 to 220 us.  Tried and not
+// faster: fewer warps with more registers each, out by warps of its own, two
+// accumulators for out, A S ahead of P, W in blocks of 32 columns (spills), S with
+// its next columns on their way.
 #include <cuda.h>
 
 #include <algorithm>
