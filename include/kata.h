@@ -481,8 +481,8 @@ kata_status_t kata_decode_step_sg(const void* q, const void* k, const void* v, v
  * tokens may reach all rows of their 128 tokens' chunk and the chunks after;
  * no other sequence's.  o must not overlap q, k or v.
  * workspace: kata_fwd_linear_decay_workspace_size() bytes (0 for short
- * calls: NULL allowed), 256-byte aligned.  Repeated calls give bitwise the
- * same result.
+ * calls: NULL allowed), 256-byte aligned; calls that may run at the same time
+ * need one each.  Repeated calls give bitwise the same result.
  */
 size_t kata_fwd_linear_decay_workspace_size(int T, int H, int d, int dv, int N);
 kata_status_t kata_fwd_linear_decay(const void* q, const void* k, const void* v, void* o,

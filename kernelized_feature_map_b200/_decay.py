@@ -50,6 +50,8 @@ def kata_fwd_linear_decay(q, k, v, log_decay, cu_seqlens=None, scale=1.0, S0=Non
     dimensions of q, k, v and o are dense; the stride between tokens is free (a
     multiple of 16 bytes), so the parts of a fused projection go in as they
     are.  All tensors are on one device, which need not be the current one.
+    With stream (a torch.cuda.Stream) the call runs there instead of on the
+    current stream, and what it allocates belongs to that stream.
     """
     return (_native or _load()).fwd(q, k, v, log_decay, cu_seqlens, scale, S0, S_out, slots, resume, return_state,
                                     zero_outside, o, workspace, stream)
@@ -97,6 +99,8 @@ def kata_attention_linear_decay(q, k, v, log_decay, cu_seqlens=None, scale=1.0, 
     the first graph that is alive, and refuses the capture otherwise."""
     if isinstance(log_decay, torch.Tensor) and log_decay.requires_grad:
         raise ValueError("log_decay gets no gradient: pass log_decay.detach()")
+    if S0 is not None and S0.shape[0] != (1 if cu_seqlens is None else cu_seqlens.shape[0] - 1):
+        raise ValueError("S0 must have one state for each sequence")
     return KataAttentionLinearDecay.apply(q, k, v, log_decay, cu_seqlens, scale, S0, return_state)
 
 

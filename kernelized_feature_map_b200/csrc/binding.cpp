@@ -13,7 +13,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -121,12 +120,24 @@ c10::cuda::CUDAStream stream_of(PyObject* o, at::Device device) {
   return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(ptr), device.index());
 }
 
+// A call's device, and its stream as the current one, so that what the call
+// allocates belongs to that stream: from another stream's pool it could still be
+// read there, by work that was queued before its owner let it go.
+struct CallGuard {
+  c10::cuda::CUDAGuard device;
+  c10::cuda::CUDAStream stream;
+  c10::cuda::OptionalCUDAStreamGuard current;
+  CallGuard(c10::Device d, PyObject* stream_arg) : device(d), stream(stream_of(stream_arg, d)) {
+    if (stream_arg != Py_None) current.reset_stream(stream);
+  }
+};
+
 // The caller's workspace, or one that the allocator keeps until the stream is past the call.
 struct Workspace {
   Tensor held;
   void* ptr = nullptr;
   size_t bytes = 0;
-  Workspace(PyObject* o, size_t need, at::Device device, PyObject* stream_arg, const c10::cuda::CUDAStream& stream) {
+  Workspace(PyObject* o, size_t need, at::Device device) {
     if (o != Py_None) {
       const Tensor& t = tensor(o, "workspace");
       TORCH_CHECK_VALUE(t.device() == device && t.is_contiguous(), "workspace must be a contiguous CUDA tensor on ",
@@ -135,7 +146,6 @@ struct Workspace {
       bytes = t.nbytes();
     } else if (need) {
       held = empty({(int64_t)need}, at::kByte, device);
-      if (stream_arg != Py_None) c10::cuda::CUDACachingAllocator::recordStream(held.storage().data_ptr(), stream);
       ptr = held.data_ptr();
       bytes = need;
     }
@@ -190,7 +200,7 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     n_slots = N;
   }
   const int64_t state[4] = {n_slots, c.H, c.d, c.dv};
-  const c10::cuda::CUDAGuard guard(c.device);
+  const CallGuard guard(c.device, a[14]);
   float* S0 = static_cast<float*>(optional(a[6], "S0", at::kFloat, state, c.device));
   float* S_out = static_cast<float*>(optional(a[7], "S_out", at::kFloat, state, c.device));
   const int64_t fresh[4] = {N, c.H, c.d, c.dv};
@@ -208,13 +218,12 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int* slots = static_cast<const int*>(optional(a[8], "slots", at::kInt, {N}, c.device));
   const unsigned char* resume = static_cast<const unsigned char*>(optional(a[9], "resume", at::kByte, {N}, c.device));
   const float scale = number(a[5]);
-  const auto stream = stream_of(a[14], c.device);
   // a state pool that is allocated here has a row for each sequence; S0 may have more
-  const Workspace ws(a[13], kata_fwd_linear_decay_workspace_size(c.n, c.H, c.d, c.dv, N), c.device, a[14], stream);
+  const Workspace ws(a[13], kata_fwd_linear_decay_workspace_size(c.n, c.H, c.d, c.dv, N), c.device);
   check("kata_fwd_linear_decay",
         kata_fwd_linear_decay(q.ptr, k.ptr, v.ptr, o.ptr, c.n, c.H, c.d, c.dv, q.stride, k.stride, v.stride, o.stride,
                               decay, scale, cu, N, S0, S_out, slots, narrow(n_slots, "n_slots"), resume, zero_outside,
-                              c.code, ws.ptr, ws.bytes, stream.stream()));
+                              c.code, ws.ptr, ws.bytes, guard.stream.stream()));
   PyObject* out;
   if (a[12] == Py_None) {
     out = THPVariable_Wrap(std::move(held_o));
@@ -254,17 +263,16 @@ PyObject* bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* dS = static_cast<const float*>(optional(a[8], "dS_out", at::kFloat, state, c.device));
   const bool return_dS0 = truth(a[9]);
   const float scale = number(a[6]);
-  const c10::cuda::CUDAGuard guard(c.device);
-  const auto stream = stream_of(a[11], c.device);
+  const CallGuard guard(c.device, a[11]);
   Tensor dq = empty({c.n, c.H, c.d}, c.type, c.device), dk = empty({c.n, c.H, c.d}, c.type, c.device);
   Tensor dv = empty({c.n, c.H, c.dv}, c.type, c.device), dS0;
   if (return_dS0) dS0 = empty(state, at::kFloat, c.device);
-  const Workspace ws(a[10], kata_bwd_linear_decay_workspace_size(c.n, c.H, c.d, c.dv, N), c.device, a[11], stream);
+  const Workspace ws(a[10], kata_bwd_linear_decay_workspace_size(c.n, c.H, c.d, c.dv, N), c.device);
   check("kata_bwd_linear_decay",
         kata_bwd_linear_decay(q.ptr, k.ptr, v.ptr, dO, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), c.n, c.H, c.d, c.dv,
                               q.stride, k.stride, v.stride, decay, scale, cu, N, S0, dS,
                               return_dS0 ? static_cast<float*>(dS0.data_ptr()) : nullptr, c.code, ws.ptr, ws.bytes,
-                              stream.stream()));
+                              guard.stream.stream()));
   PyObject* out = PyTuple_New(return_dS0 ? 4 : 3);
   if (!out) throw python_error();
   PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(std::move(dq)));
@@ -288,15 +296,14 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* decay = static_cast<const float*>(dense(a[4], "log_decay", at::kFloat, {c.H}, c.device));
   const int* slots = static_cast<const int*>(optional(a[5], "slots", at::kInt, {c.n}, c.device));
   const float scale = number(a[6]);
-  const c10::cuda::CUDAGuard guard(c.device);
-  const auto stream = stream_of(a[8], c.device);
+  const CallGuard guard(c.device, a[8]);
   Tensor held;
   if (a[7] == Py_None) held = empty({c.n, c.H, c.dv}, c.type, c.device);
   const Tensor& ot = a[7] == Py_None ? held : tensor(a[7], "o");
   const Rows o = rows(ot, "o", c.type, c.n, c.H, c.dv, c.device);
   check("kata_decode_step_linear_decay",
         kata_decode_step_linear_decay(q.ptr, k.ptr, v.ptr, o.ptr, S, c.n, c.H, c.d, c.dv, q.stride, k.stride, v.stride,
-                                      o.stride, decay, scale, slots, n_slots, c.code, stream.stream()));
+                                      o.stride, decay, scale, slots, n_slots, c.code, guard.stream.stream()));
   if (a[7] == Py_None) return THPVariable_Wrap(std::move(held));
   Py_INCREF(a[7]);
   return a[7];
@@ -345,10 +352,10 @@ PyObject* store(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 8);
   const Pools p = pools(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
-  const c10::cuda::CUDAGuard guard(p.device);
+  const CallGuard guard(p.device, a[7]);
   check("kata_state_store_q8",
         kata_state_store_q8(p.S, p.z, p.n_slots, p.cache, p.scale, p.z_cache, p.n_entries, p.slots, p.entries, p.n, p.H,
-                            p.rows, p.dv, stream_of(a[7], p.device).stream()));
+                            p.rows, p.dv, guard.stream.stream()));
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -358,10 +365,10 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 8);
   const Pools p = pools(a[2], a[0], a[1], a[4], a[3], a[5], a[6]);
-  const c10::cuda::CUDAGuard guard(p.device);
+  const CallGuard guard(p.device, a[7]);
   check("kata_state_load_q8",
         kata_state_load_q8(p.cache, p.scale, p.z_cache, p.n_entries, p.S, p.z, p.n_slots, p.entries, p.slots, p.n, p.H,
-                           p.rows, p.dv, stream_of(a[7], p.device).stream()));
+                           p.rows, p.dv, guard.stream.stream()));
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

@@ -202,3 +202,12 @@ def test_binding_refuses_host_tensors():
             call()
     with pytest.raises(ValueError):
         K.kata_attention_linear_decay(x, x, x, g.requires_grad_())
+
+
+def test_attention_needs_a_state_for_each_sequence():
+    import kernelized_feature_map_b200 as K
+    x = torch.zeros(8, 1, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 5, 8], dtype=torch.int32)
+    for states, edges in ((3, cu), (1, cu), (2, None)):
+        with pytest.raises(ValueError, match="one state for each sequence"):
+            K.kata_attention_linear_decay(x, x, x, torch.zeros(1), edges, S0=torch.zeros(states, 1, 64, 64))

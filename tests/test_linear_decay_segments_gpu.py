@@ -306,3 +306,33 @@ def test_chain_of_launches_that_overlap():
         got = run(False)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("call", ["prompt", "gradients", "step"])
+def test_what_a_given_stream_writes_is_its_own(call):
+    """A call on another stream than the current one gets no memory that work
+    queued on the current one still reads (a block let go there may be handed
+    out again there at once, but not elsewhere)."""
+    r, T, H, d = gen(31), 512, 16, 128
+    q, k, v, dO = (bf(r, T, H, d) for _ in range(4))
+    g, S = decays(H), torch.zeros(2, T, H, d, d, device="cuda") if call == "step" else None
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def run(pool, **kw):
+        if call == "prompt":
+            return K.kata_fwd_linear_decay(q, k, v, g, scale=0.1, return_state=True, **kw)
+        if call == "gradients":
+            return K.kata_bwd_linear_decay(q, k, v, dO, g, scale=0.1, return_dS0=True, **kw)
+        return (K.kata_decode_step_linear_decay(q, k, v, S[pool], g, scale=0.1, **kw),)
+
+    want = run(0)
+    blocks = [torch.full_like(t, 3.0) for t in want]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    copies = [b.clone() for b in blocks]
+    del blocks
+    got = run(1, stream=other)
+    torch.cuda.synchronize()
+    assert all(bool((c == 3.0).all()) for c in copies)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
