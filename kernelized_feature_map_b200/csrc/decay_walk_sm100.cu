@@ -55,8 +55,9 @@
 // works 38%; its tiles cross shared memory in 4700 cycles, and at 148 SMs its
 // bytes HBM in 5500.  The sums, of which no chunk waits for another, are bound by
 // the loads in flight (three stages 4.6 TB/s, two 3.7).  Measured: 131072 tokens,
-// 16 heads, d = dv = 128 670 to 710 us, 3.2 TB/s of q, k, v and o; a quarter of it
-// are the segments' sums, which read k and v once more.  8192 tokens in 13
+// 16 heads, d = dv = 128 650 to 710 us, 3.2 TB/s of q, k, v and o (780 us among
+// other work, under the power cap); a quarter of it are the segments' sums, which
+// read k and v once more.  8192 tokens in 13
 // sequences: 81 us.  75 tokens, d = dv = 64: 8.3 us, a launch and one chunk's path.
 // Gradients, 8 x 2048 tokens, 16 heads, d = dv = 128: 190 to 220 us.  Tried and not
 // faster: fewer warps with more registers each, out by warps of its own, two
