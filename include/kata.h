@@ -470,7 +470,7 @@ kata_status_t kata_decode_step_sg(const void* q, const void* k, const void* v, v
  * negative slot starts from zero and leaves no state.  resume (NULL: all of
  * them) holds N bytes on the device: a sequence with 0 starts from zero
  * though S0 is given.  S0 and S_out may be the same pool, otherwise they must not
- * overlap.  A slot of n_slots or more, and with S_out a slot that an earlier
+ * overlap (without slots: their first N rows must not).  A slot of n_slots or more, and with S_out a slot that an earlier
  * sequence of the call names too, records KATA_ERR_INVALID_ARG and counts
  * as negative.  A sequence of length 0 leaves the state it starts from.
  * bf16; d and dv in {64, 128}; others KATA_ERR_UNSUPPORTED.  Tensor-core

@@ -218,7 +218,8 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int* slots = static_cast<const int*>(optional(a[8], "slots", at::kInt, {N}, c.device));
   const unsigned char* resume = static_cast<const unsigned char*>(optional(a[9], "resume", at::kByte, {N}, c.device));
   const float scale = number(a[5]);
-  // a state pool that is allocated here has a row for each sequence; S0 may have more
+  // a state pool that is allocated here has a row for each sequence, S0 may have more: without slots only the
+  // first N rows of either are the call's
   const Workspace ws(a[13], kata_fwd_linear_decay_workspace_size(c.n, c.H, c.d, c.dv, N), c.device);
   check("kata_fwd_linear_decay",
         kata_fwd_linear_decay(q.ptr, k.ptr, v.ptr, o.ptr, c.n, c.H, c.d, c.dv, q.stride, k.stride, v.stride, o.stride,

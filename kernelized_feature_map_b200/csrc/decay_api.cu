@@ -78,7 +78,8 @@ KATA_API kata_status_t kata_fwd_linear_decay(const void* q, const void* k, const
     if (!aligned(p, 16)) return KATA_ERR_MISALIGNED;
   for (const void* p : {(const void*)log_decay, (const void*)cu_seqlens, (const void*)slots})
     if (!aligned(p, 4)) return KATA_ERR_MISALIGNED;
-  if (S0 != S_out && overlap(S0, S_out, (size_t)n_slots * H * d * dv)) return KATA_ERR_INVALID_ARG;
+  // without slots the call's states are the first N of either pool
+  if (S0 != S_out && overlap(S0, S_out, (size_t)(slots ? n_slots : N) * H * d * dv)) return KATA_ERR_INVALID_ARG;
   const DecayWalk w{q, k, v, o, q_stride, k_stride, v_stride, o_stride, d, dv, false, S0, false, S_out};
   const DecayShape sh{T, H, N, cu_seqlens, log_decay, scale, slots, n_slots, resume, zero_outside != 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);

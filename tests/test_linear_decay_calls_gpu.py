@@ -1,0 +1,55 @@
+"""Linear attention with a per-head decay and the 8-bit state cache: calls that
+the documentation allows and that the other tests leave out."""
+import numpy as np
+import pytest
+import torch
+
+import kernelized_feature_map_b200 as K
+from kernelized_feature_map_b200 import _abi
+from oracle import linear_decay as od
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    from kernelized_feature_map_b200 import build
+    build.build()
+    torch.cuda.synchronize()
+    K.kata_get_status()
+    yield
+    torch.cuda.synchronize()
+    assert K.kata_get_status() == _abi.KATA_OK
+
+
+def gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def bf(g, *shape):
+    return torch.randn(shape, device="cuda", generator=g).to(torch.bfloat16)
+
+
+def edges(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("lens", [[30, 170], [5000, 200]])
+def test_a_fresh_state_for_each_sequence_from_a_larger_pool(lens):
+    """S0 has more states than the call has sequences, and what the call allocates for S_out can lie right below it
+    (where the allocator cuts both from the start of a free block)."""
+    r, H, d, N = gen(0), 16, 128, len(lens)
+    T, g, cu = sum(lens), torch.linspace(-0.5, 0, H, device="cuda"), edges(lens)
+    q, k, v = (bf(r, T, H, d) for _ in range(3))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    block = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    del block
+    below = torch.empty(N, H, d, d, device="cuda")
+    S0 = torch.randn(N + 29, H, d, d, device="cuda", generator=r)
+    few = S0[:N].clone()
+    del below
+    o, S = K.kata_fwd_linear_decay(q, k, v, g, cu, 0.1, S0=S0, return_state=True)
+    assert S.shape == (N, H, d, d)
+    want_o, want = K.kata_fwd_linear_decay(q, k, v, g, cu, 0.1, S0=few, return_state=True)
+    assert torch.equal(S, want) and torch.equal(o, want_o)
