@@ -49,17 +49,18 @@ __device__ __forceinline__ float row_scale(float max) {
 // |x| <= 127 s (1 + 2^-24) and s >= 2^-126.  Added to 1.5 2^23, x / s (times an
 // approximate 1 / s) is rounded to an integer q; the remainder x - q s has no
 // more than 24 bits, so the fma gives it exactly, and below s / 2 it proves q the
-// nearest.  Otherwise, next to a border, q is one off or x / s a tie.
+// nearest.  Otherwise, next to a border, q is one off or x / s a tie.  Twice the
+// remainder is compared with s: half of an odd s below 2^-125 is no fp32 value.
 constexpr float kMagic = 12582912.f;
 struct Rounded {
-  float t, r;
+  float t, r2;  // r2: twice the remainder
   __device__ __forceinline__ Rounded(float x, float s, float inv) {
     t = fmaf(x, inv, kMagic);
-    r = fmaf(-(t - kMagic), s, x);
+    r2 = 2.f * fmaf(-(t - kMagic), s, x);
   }
   __device__ __forceinline__ void settle(float s) {
-    const float h = 0.5f * s, a = fabsf(r);
-    if (a > h || (a == h && (__float_as_uint(t) & 1u))) t += r > 0.f ? 1.f : -1.f;
+    const float a = fabsf(r2);
+    if (a > s || (a == s && (__float_as_uint(t) & 1u))) t += r2 > 0.f ? 1.f : -1.f;
   }
 };
 
@@ -121,8 +122,8 @@ __global__ void __launch_bounds__(kThreads)
     const bool held = m < 0x7f800000u && s >= FLT_MIN;
     const float inv = __frcp_rn(held ? s : 1.f);
     Rounded v[4] = {{x[u].x, s, inv}, {x[u].y, s, inv}, {x[u].z, s, inv}, {x[u].w, s, inv}};
-    const float worst = fmaxf(fmaxf(fabsf(v[0].r), fabsf(v[1].r)), fmaxf(fabsf(v[2].r), fabsf(v[3].r)));
-    if (__any_sync(0xffffffffu, worst >= 0.5f * s)) {
+    const float worst = fmaxf(fmaxf(fabsf(v[0].r2), fabsf(v[1].r2)), fmaxf(fabsf(v[2].r2), fabsf(v[3].r2)));
+    if (__any_sync(0xffffffffu, worst >= s)) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e].settle(s);
     }

@@ -53,3 +53,26 @@ def test_a_fresh_state_for_each_sequence_from_a_larger_pool(lens):
     assert S.shape == (N, H, d, d)
     want_o, want = K.kata_fwd_linear_decay(q, k, v, g, cu, 0.1, S0=few, return_state=True)
     assert torch.equal(S, want) and torch.equal(o, want_o)
+
+
+def test_q8_rows_at_the_smallest_scales_are_exact():
+    """Scales in [2^-126, 2^-125) with an odd significand, whose half is no fp32 value, and values on or next to the
+    borders between two integers."""
+    r = np.random.default_rng(3)
+    rows, dv = 4096, 64
+    x = np.zeros((rows, dv), np.float32)
+    unit = 2.0 ** -149  # every value and scale here is a multiple of it
+    for i in range(rows):
+        s = (1 << 23) + 2 * int(r.integers(0, 1 << 22)) + 1
+        k = r.integers(-126, 126, dv)
+        y = ((2 * k + 1) * s) // 2 + r.integers(-1, 3, dv)  # (k + 1/2) s is an integer and a half
+        x[i] = (y * unit).astype(np.float32)
+        x[i, 0] = np.float32(127 * s * unit)
+    c, s = od.store_q8(x)
+    assert ((s >= 2.0 ** -126) & (s < 2.0 ** -125)).all() and (np.round(s / unit) % 2 == 1).mean() > 0.3
+    cache = torch.empty((1, 1, rows, dv), dtype=torch.int8, device="cuda")
+    scale = torch.empty((1, 1, rows), device="cuda")
+    K.kata_state_store_q8(torch.from_numpy(x).cuda().view(1, 1, rows, dv), cache, scale)
+    assert np.array_equal(scale.cpu().numpy()[0, 0], s)
+    wrong = np.argwhere(cache.cpu().numpy()[0, 0] != c)
+    assert not len(wrong), (len(wrong), wrong[:3])
