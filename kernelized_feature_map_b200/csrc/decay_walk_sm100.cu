@@ -1160,16 +1160,21 @@ __global__ void __launch_bounds__(kScanThreads) decay_scan_kernel(const __grid_c
   }
 }
 
-// fin = init or zero, for sequences without tokens (T = 0)
-__global__ void __launch_bounds__(256) decay_empty_kernel(const float* init, float* fin, const int* slots, int n_slots,
-                                                          const unsigned char* resume, long long size4, int* status) {
+// fin = init or zero, for sequences without tokens (T = 0); the states of many
+// heads are more tiles than a grid has rows
+constexpr int kEmptyThreads = 256, kMaxGridRows = 65535;
+
+__global__ void __launch_bounds__(kEmptyThreads) decay_empty_kernel(const float* init, float* fin, const int* slots,
+                                                                    int n_slots, const unsigned char* resume,
+                                                                    long long size4, int* status) {
   const int n = blockIdx.x;
   const int row = pool_row(slots, n, n_slots, true, threadIdx.x & 31, status);
-  const long long x = (long long)blockIdx.y * 256 + threadIdx.x;
-  if (row < 0 || x >= size4) return;
+  if (row < 0) return;
   const bool entered = init && (!resume || resume[n]);
-  reinterpret_cast<float4*>(fin)[row * size4 + x] =
-      entered ? reinterpret_cast<const float4*>(init)[row * size4 + x] : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (long long x = (long long)blockIdx.y * kEmptyThreads + threadIdx.x; x < size4;
+       x += (long long)gridDim.y * kEmptyThreads)
+    reinterpret_cast<float4*>(fin)[row * size4 + x] =
+        entered ? reinterpret_cast<const float4*>(init)[row * size4 + x] : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // [T][H][width] with `stride` elements between tokens, box [128 tokens][1 head][64 values], 128-byte swizzle
@@ -1322,8 +1327,9 @@ cudaError_t launch_decay_walks(const DecayWalk* walks, int n, const DecayShape& 
 cudaError_t launch_decay_empty(const DecayWalk& w, const DecayShape& sh, const WaitCtl& wc, cudaStream_t st) {
   if (!w.fin) return cudaSuccess;
   const long long size4 = (long long)sh.H * w.d1 * w.d2 / 4;
-  decay_empty_kernel<<<dim3((unsigned)sh.N, (unsigned)((size4 + 255) / 256)), 256, 0, st>>>(
-      w.init, w.fin, sh.slots, sh.n_slots, sh.resume, size4, wc.status);
+  const long long tiles = std::min((size4 + kEmptyThreads - 1) / kEmptyThreads, (long long)kMaxGridRows);
+  decay_empty_kernel<<<dim3((unsigned)sh.N, (unsigned)tiles), kEmptyThreads, 0, st>>>(w.init, w.fin, sh.slots, sh.n_slots,
+                                                                                      sh.resume, size4, wc.status);
   return cudaGetLastError();
 }
 

@@ -76,3 +76,16 @@ def test_q8_rows_at_the_smallest_scales_are_exact():
     assert np.array_equal(scale.cpu().numpy()[0, 0], s)
     wrong = np.argwhere(cache.cpu().numpy()[0, 0] != c)
     assert not len(wrong), (len(wrong), wrong[:3])
+
+
+def test_no_tokens_at_the_largest_number_of_heads():
+    H, d = 4096, 128
+    empty = [torch.empty(0, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    S0 = torch.randn(1, H, d, d, device="cuda", generator=gen(1))
+    g = torch.zeros(H, device="cuda")
+    _, S = K.kata_fwd_linear_decay(*empty[:3], g, S0=S0, return_state=True)
+    assert torch.equal(S, S0)
+    dS0 = K.kata_bwd_linear_decay(*empty, g, dS_out=S0, return_dS0=True)[3]
+    assert torch.equal(dS0, S0)
+    _, S = K.kata_fwd_linear_decay(*empty[:3], g, return_state=True)
+    assert not S.any()
