@@ -109,6 +109,16 @@ Tensor empty(at::IntArrayRef shape, ScalarType type, at::Device device) {
   return Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
+// Tensors of the caller that a call has written: torch's version counter says so to autograd, which refuses a backward
+// pass whose saved tensors were written since.  (Inference tensors have none.)
+void written(std::initializer_list<PyObject*> tensors) {
+  for (PyObject* o : tensors) {
+    if (o == Py_None) continue;
+    const Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+}
+
 // The stream of a call: the one that was given, or the device's current one.
 c10::cuda::CUDAStream stream_of(PyObject* o, at::Device device) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device.index());
@@ -225,6 +235,7 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         kata_fwd_linear_decay(q.ptr, k.ptr, v.ptr, o.ptr, c.n, c.H, c.d, c.dv, q.stride, k.stride, v.stride, o.stride,
                               decay, scale, cu, N, S0, S_out, slots, narrow(n_slots, "n_slots"), resume, zero_outside,
                               c.code, ws.ptr, ws.bytes, guard.stream.stream()));
+  written({a[7], a[12]});
   PyObject* out;
   if (a[12] == Py_None) {
     out = THPVariable_Wrap(std::move(held_o));
@@ -305,6 +316,7 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check("kata_decode_step_linear_decay",
         kata_decode_step_linear_decay(q.ptr, k.ptr, v.ptr, o.ptr, S, c.n, c.H, c.d, c.dv, q.stride, k.stride, v.stride,
                                       o.stride, decay, scale, slots, n_slots, c.code, guard.stream.stream()));
+  written({a[3], a[7]});
   if (a[7] == Py_None) return THPVariable_Wrap(std::move(held));
   Py_INCREF(a[7]);
   return a[7];
@@ -357,6 +369,7 @@ PyObject* store(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check("kata_state_store_q8",
         kata_state_store_q8(p.S, p.z, p.n_slots, p.cache, p.scale, p.z_cache, p.n_entries, p.slots, p.entries, p.n, p.H,
                             p.rows, p.dv, guard.stream.stream()));
+  written({a[1], a[2], a[6]});
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -370,6 +383,7 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check("kata_state_load_q8",
         kata_state_load_q8(p.cache, p.scale, p.z_cache, p.n_entries, p.S, p.z, p.n_slots, p.entries, p.slots, p.n, p.H,
                            p.rows, p.dv, guard.stream.stream()));
+  written({a[2], a[5]});
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

@@ -89,3 +89,40 @@ def test_no_tokens_at_the_largest_number_of_heads():
     assert torch.equal(dS0, S0)
     _, S = K.kata_fwd_linear_decay(*empty[:3], g, return_state=True)
     assert not S.any()
+
+
+def test_what_a_call_writes_is_known_to_autograd():
+    """A state saved for a backward pass and written since is an error there, as with torch's own operations, and not
+    a wrong gradient; what is only read keeps its version."""
+    r, H, d = gen(2), 2, 64
+    x, g = bf(r, 5, H, d), torch.full((H,), -0.1, device="cuda")
+    S = torch.randn(3, H, d, d, device="cuda", generator=r)
+    z, zc, sc = torch.zeros(3, H, d, device="cuda"), torch.zeros(3, H, d, device="cuda"), torch.zeros(3, H, d, device="cuda")
+    cache, o = torch.zeros(3, H, d, d, dtype=torch.int8, device="cuda"), torch.zeros_like(x)
+    calls = [
+        (lambda: K.kata_fwd_linear_decay(x, x, x, g, S0=S, return_state=True), []),
+        (lambda: K.kata_fwd_linear_decay(x, x, x, g, S0=S, S_out=S, o=o), [S, o]),
+        (lambda: K.kata_decode_step_linear_decay(x[:3], x[:3], x[:3], S, g), [S]),
+        (lambda: K.kata_decode_step_linear_decay(x[:3], x[:3], x[:3], S, g, o=o[:3]), [S, o]),
+        (lambda: K.kata_state_store_q8(S, cache, sc, z=z, z_cache=zc), [cache, sc, zc]),
+        (lambda: K.kata_state_load_q8(cache, sc, S, z=z, z_cache=zc), [S, z]),
+        (lambda: K.kata_bwd_linear_decay(x, x, x, x, g, S0=S[:1], dS_out=S[:1]), []),
+    ]
+    every = [x, g, S, z, zc, sc, cache, o]
+    for call, wrote in calls:
+        before = [t._version for t in every]
+        call()
+        for t, v in zip(every, before):
+            assert (t._version > v) == any(t is w for w in wrote)
+    q, k, v = (bf(r, 5, H, d).requires_grad_() for _ in range(3))
+    S0 = torch.randn(1, H, d, d, device="cuda", generator=r)
+    y = K.kata_attention_linear_decay(q, k, v, g, S0=S0)
+    K.kata_decode_step_linear_decay(x[:1], x[:1], x[:1], S0, g)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():
+        T = torch.zeros(3, H, d, d, device="cuda")
+    K.kata_decode_step_linear_decay(x[:3], x[:3], x[:3], T, g)  # inference tensors have no version
+    with torch.inference_mode():
+        K.kata_decode_step_linear_decay(x[:3], x[:3], x[:3], T, g)
+    assert T.any()
