@@ -132,6 +132,12 @@ def _opt(t, name):
     return None if t is None else _dev(t, name)
 
 
+def _written(*tensors):
+    """Tell autograd what a call has written: a backward pass whose saved
+    tensors were written since is an error then, not a wrong gradient."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def kata_fwd_quadratic(q, k, v, o=None, stream=None):
     """Flash-style O(T^2) forward.  q,k [B,H,T,p], v [B,H,T,dv] -> o [B,H,T,dv]."""
     B, H, T, p = q.shape
@@ -140,6 +146,7 @@ def kata_fwd_quadratic(q, k, v, o=None, stream=None):
         o = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
     _check("kata_fwd_quadratic", lib().kata_fwd_quadratic(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, p, dv, _dtype_code(q), _stream_ptr(stream)))
+    _written(o)
     return o
 
 
@@ -172,6 +179,7 @@ def kata_fwd_chunked(q, k, v, C=64, S0=None, z0=None, return_state=False, o=None
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, p, dv, C, _dtype_code(q),
         _opt(S0, "S0"), _opt(z0, "z0"), _opt(S_out, "S_out"), _opt(z_out, "z_out"),
         _opt(workspace, "workspace"), ws_bytes, _stream_ptr(stream)))
+    _written(o, S_out, z_out)
     if return_state:
         return o, S_out, z_out
     return o
@@ -202,6 +210,7 @@ def kata_fwd_chunked_noalloc(q, k, v, C=64, S0=None, z0=None, return_state=False
     _check("kata_fwd_chunked_noalloc", lib().kata_fwd_chunked_noalloc(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, p, dv, C, _dtype_code(q),
         _opt(S0, "S0"), _opt(z0, "z0"), _opt(S_out, "S_out"), _opt(z_out, "z_out"), _stream_ptr(stream)))
+    _written(o, S_out, z_out)
     if return_state:
         return o, S_out, z_out
     return o
@@ -222,6 +231,7 @@ def kata_fwd_chunked_sequential(q, k, v, C=64, S0=None, z0=None, return_state=Fa
     _check("kata_fwd_chunked_sequential", lib().kata_fwd_chunked_sequential(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, p, dv, C, _dtype_code(q),
         _opt(S0, "S0"), _opt(z0, "z0"), _opt(S_out, "S_out"), _opt(z_out, "z_out"), _stream_ptr(stream)))
+    _written(o, S_out, z_out)
     if return_state:
         return o, S_out, z_out
     return o
@@ -255,6 +265,7 @@ def kata_fwd_linear_chunked(q, k, v, C=64, S0=None, z0=None, return_state=False,
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, d, dv, C, _dtype_code(q),
         _opt(S0, "S0"), _opt(z0, "z0"), _opt(S_out, "S_out"), _opt(z_out, "z_out"),
         _opt(workspace, "workspace"), ws_bytes, _stream_ptr(stream)))
+    _written(o, S_out, z_out)
     if return_state:
         return o, S_out, z_out
     return o
@@ -275,6 +286,7 @@ def kata_fwd_linear_chunked_sequential(q, k, v, C=64, S0=None, z0=None, return_s
     _check("kata_fwd_linear_chunked_sequential", lib().kata_fwd_linear_chunked_sequential(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, d, dv, C, _dtype_code(q),
         _opt(S0, "S0"), _opt(z0, "z0"), _opt(S_out, "S_out"), _opt(z_out, "z_out"), _stream_ptr(stream)))
+    _written(o, S_out, z_out)
     if return_state:
         return o, S_out, z_out
     return o
@@ -289,6 +301,7 @@ def kata_decode_step(q, k, v, S, z, o=None, stream=None):
     _check("kata_decode_step", lib().kata_decode_step(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), _dev(S, "S"), _dev(z, "z"), B, H, p, dv,
         _dtype_code(q), _stream_ptr(stream)))
+    _written(o, S, z)
     return o
 
 
@@ -306,6 +319,7 @@ def kata_fwd_quadratic_train(q, k, v, o=None, D=None, stream=None):
     _check("kata_fwd_quadratic_train", lib().kata_fwd_quadratic_train(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), _dev(D, "D"), B, H, T, p, dv, _dtype_code(q),
         _stream_ptr(stream)))
+    _written(o, D)
     return o, D
 
 
@@ -367,6 +381,7 @@ def kata_fwd_sg_quadratic(q, k, v, groups, layout="bhtd", o=None, stream=None):
     _check("kata_fwd_sg_quadratic", lib().kata_fwd_sg_quadratic(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, d, int(groups), dv, code,
         _dtype_code(q), _stream_ptr(stream)))
+    _written(o)
     return o
 
 
@@ -386,6 +401,7 @@ def kata_fwd_chunked_train(q, k, v, C=64, o=None, D=None, workspace=None, stream
     _check("kata_fwd_chunked_train", lib().kata_fwd_chunked_train(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), _dev(D, "D"), B, H, T, p, dv, C, _dtype_code(q),
         _opt(workspace, "workspace"), ws_bytes, _stream_ptr(stream)))
+    _written(o, D)
     return o, D
 
 
@@ -438,6 +454,7 @@ def kata_fwd_mg_quadratic_train(q, k, v, groups, o=None, D=None, stream=None):
     _check("kata_fwd_mg_quadratic_train", lib().kata_fwd_mg_quadratic_train(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), _dev(D, "D"), B, H, T, d, int(groups), dv,
         _dtype_code(q), _stream_ptr(stream)))
+    _written(o, D)
     return o, D
 
 
@@ -492,6 +509,7 @@ def kata_fwd_sg_quadratic_train(q, k, v, groups, o=None, D=None, stream=None):
     _check("kata_fwd_sg_quadratic_train", lib().kata_fwd_sg_quadratic_train(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), _dev(D, "D"), B, H, T, d, int(groups), dv,
         _dtype_code(q), _stream_ptr(stream)))
+    _written(o, D)
     return o, D
 
 
@@ -557,6 +575,7 @@ def kata_fwd_mg_quadratic(q, k, v, groups, layout="bhtd", o=None, stream=None):
     _check("kata_fwd_mg_quadratic", lib().kata_fwd_mg_quadratic(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, d, int(groups), dv, code,
         _dtype_code(q), _stream_ptr(stream)))
+    _written(o)
     return o
 
 
@@ -600,6 +619,7 @@ def kata_fwd_mg_chunked(q, k, v, groups, C=64, layout="bhtd", S0=None, z0=None, 
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, d, g, dv, C, code, _dtype_code(q),
         _opt(S0, "S0"), _opt(z0, "z0"), _opt(S_out, "S_out"), _opt(z_out, "z_out"),
         _opt(workspace, "workspace"), ws_bytes, _stream_ptr(stream)))
+    _written(o, S_out, z_out)
     if return_state:
         return o, S_out, z_out
     return o
@@ -621,6 +641,7 @@ def kata_decode_step_mg(q, k, v, S, z, groups, o=None, stream=None):
     _check("kata_decode_step_mg", lib().kata_decode_step_mg(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), _dev(S, "S"), _dev(z, "z"), B, H, d, int(groups),
         dv, _dtype_code(q), _stream_ptr(stream)))
+    _written(o, S, z)
     return o
 
 
@@ -650,6 +671,7 @@ def kata_fwd_sg_chunked(q, k, v, groups, C=64, S0=None, z0=None, return_state=Fa
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), B, H, T, d, int(groups), dv, C, _dtype_code(q),
         _opt(S0, "S0"), _opt(z0, "z0"), _opt(S_out, "S_out"), _opt(z_out, "z_out"),
         _opt(workspace, "workspace"), ws_bytes, _stream_ptr(stream)))
+    _written(o, S_out, z_out)
     if return_state:
         return o, S_out, z_out
     return o
@@ -666,6 +688,7 @@ def kata_decode_step_sg(q, k, v, S, z, groups, o=None, stream=None):
     _check("kata_decode_step_sg", lib().kata_decode_step_sg(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(o, "o"), _dev(S, "S"), _dev(z, "z"), B, H, d, int(groups),
         dv, _dtype_code(q), _stream_ptr(stream)))
+    _written(o, S, z)
     return o
 
 
