@@ -67,6 +67,15 @@ def kata_bwd_linear_decay(q, k, v, dO, log_decay, cu_seqlens=None, scale=1.0, S0
                                     stream)
 
 
+def _upstream(g):
+    """An upstream gradient as the kernels read it: dense, from 16 bytes on (what is cut from a larger gradient, as
+    behind a concatenation, may start anywhere)."""
+    if g is None:
+        return None
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class KataAttentionLinearDecay(torch.autograd.Function):
     """Autograd wrapper of kata_fwd_linear_decay and kata_bwd_linear_decay (marshalling only)."""
 
@@ -83,10 +92,10 @@ class KataAttentionLinearDecay(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dO, dS=None):
         q, k, v, log_decay, cu_seqlens, S0 = ctx.saved_tensors
-        dO = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if dO is None else dO.contiguous()
+        dO = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if dO is None else _upstream(dO)
         want = S0 is not None and ctx.needs_input_grad[6]
         g = kata_bwd_linear_decay(q, k, v, dO, log_decay, cu_seqlens, ctx.scale, S0=S0,
-                                  dS_out=None if dS is None else dS.contiguous(), return_dS0=want)
+                                  dS_out=_upstream(dS), return_dS0=want)
         return g[0], g[1], g[2], None, None, None, (g[3] if want else None), None
 
 

@@ -126,3 +126,18 @@ def test_what_a_call_writes_is_known_to_autograd():
     with torch.inference_mode():
         K.kata_decode_step_linear_decay(x[:3], x[:3], x[:3], T, g)
     assert T.any()
+
+
+def test_gradients_that_start_anywhere_in_memory():
+    """The outputs behind a concatenation of flat tensors: their gradients are dense, but start on 2 or 4 bytes."""
+    r, H, d, cu = gen(4), 2, 64, edges([20, 30])
+    q, k, v = (bf(r, 50, H, d).requires_grad_() for _ in range(3))
+    S0 = torch.randn(2, H, d, d, device="cuda", generator=r).requires_grad_()
+    g, leaves = torch.full((H,), -0.1, device="cuda"), (q, k, v, S0)
+    o, S = K.kata_attention_linear_decay(q, k, v, g, cu, 0.1, S0=S0, return_state=True)
+    dO, dS = bf(r, 50, H, d), torch.randn(2, H, d, d, device="cuda", generator=r)
+    want = torch.autograd.grad((o, S), leaves, (dO, dS), retain_graph=True)
+    flat = [torch.cat([torch.zeros(3, dtype=t.dtype, device="cuda"), t.flatten()]) for t in (o, S)]
+    up = [torch.cat([torch.zeros(3, dtype=t.dtype, device="cuda"), t.flatten()]) for t in (dO, dS)]
+    got = torch.autograd.grad(flat, leaves, up)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
