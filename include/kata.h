@@ -480,6 +480,10 @@ kata_status_t kata_decode_step_sg(const void* q, const void* k, const void* v, v
  * copy of the state is multiplied by q.  Infinities and NaN in a sequence's
  * tokens may reach all rows of their 128 tokens' chunk and the chunks after;
  * no other sequence's.  o must not overlap q, k or v.
+ * Sizes: T up to 2^30, H up to 4096, N up to 2^20, 3H (T/16 + N) below 2^31
+ * and N*N*H up to 2^35 (the time of a call grows with the square of its
+ * sequences: 2.4 s there); more is KATA_ERR_UNSUPPORTED, and goes into
+ * several calls.
  * workspace: kata_fwd_linear_decay_workspace_size() bytes (0 for short
  * calls: NULL allowed), 256-byte aligned; calls that may run at the same time
  * need one each.  Repeated calls give bitwise the same result.
@@ -501,8 +505,9 @@ kata_status_t kata_fwd_linear_decay(const void* q, const void* k, const void* v,
  * S0, dS_out, dS0 (NULL: not wanted): [N, H, d, dv] fp32, one row per
  * sequence.  dO, dq, dk [T, H, d] and dv are contiguous; q, k, v as in the
  * forward.  Rows outside every sequence get zero gradients.  The decays are
- * constants: they get no gradient.  Types, sizes, workspace
- * (kata_bwd_linear_decay_workspace_size()) and errors as in the forward.
+ * constants: they get no gradient.  Types, sizes (N*N*H up to 2^35 / 3),
+ * workspace (kata_bwd_linear_decay_workspace_size()) and errors as in the
+ * forward.
  */
 size_t kata_bwd_linear_decay_workspace_size(int T, int H, int d, int dv, int N);
 kata_status_t kata_bwd_linear_decay(const void* q, const void* k, const void* v, const void* dO,
@@ -521,8 +526,9 @@ kata_status_t kata_bwd_linear_decay(const void* q, const void* k, const void* v,
  * its row of o is written as zeros and no state is touched.  A slot of
  * n_slots or more, or one that an earlier stream of the call names too,
  * counts as negative and records KATA_ERR_INVALID_ARG in the status word.
- * d and dv in {64, 128}; fp32 arithmetic throughout.  o must not overlap q, k
- * or v.
+ * d and dv in {64, 128}; n up to 2^20 and with slots n*n*H*dv up to 2^46, more
+ * is KATA_ERR_UNSUPPORTED; fp32 arithmetic throughout.  o must not overlap q,
+ * k or v.
  */
 kata_status_t kata_decode_step_linear_decay(const void* q, const void* k, const void* v, void* o, float* S,
                                             int n, int H, int d, int dv,

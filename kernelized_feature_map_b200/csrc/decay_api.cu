@@ -14,8 +14,13 @@ bool width_ok(int w) { return w == 64 || w == 128; }
 // Sizes that fit the grids and the 32-bit token and index arithmetic.
 constexpr int kMaxTokens = 1 << 30, kMaxSequences = 1 << 20, kMaxHeads = 4096;
 constexpr long long kMaxStride = 1ll << 36;  // elements; a tensor map's stride is below 2^40 bytes
+// Every CTA of a walk looks for its sequence from the first on, 32 at a time, and with slots every CTA of a step for
+// an earlier stream of its slot, so that a call's time grows with their square: 16384 sequences of 16 heads take
+// 0.29 s, 32768 streams of 16 heads and dv = 64 26 ms (2.6 ms without slots).  A million of either would hold the
+// GPU for many minutes.  At these bounds the search takes 2.4 and 1.5 s.
+constexpr long long kMaxWalkSearch = 1ll << 35, kMaxStepSearch = 1ll << 41;
 
-kata_status_t check_shape(int T, int H, int d, int dv, int N, kata_dtype_t dt) {
+kata_status_t check_shape(int T, int H, int d, int dv, int N, kata_dtype_t dt, int walks) {
   if (T < 0 || H < 1 || N < 0) return KATA_ERR_INVALID_ARG;
   if (dt != KATA_BF16 && dt != KATA_F32) return KATA_ERR_INVALID_ARG;
   if (!width_ok(d) || !width_ok(dv)) return KATA_ERR_UNSUPPORTED;
@@ -23,6 +28,7 @@ kata_status_t check_shape(int T, int H, int d, int dv, int N, kata_dtype_t dt) {
   // one CTA per segment, head and walk, and up to 16 for the scan of a split sequence, with at least 256 tokens to
   // a segment
   if (((long long)T / 256 * 16 + N) * H * 3 > 0x7fffffffll) return KATA_ERR_UNSUPPORTED;
+  if ((long long)N * N * H * walks > kMaxWalkSearch) return KATA_ERR_UNSUPPORTED;
   return KATA_OK;
 }
 
@@ -49,7 +55,7 @@ bool overlap(const float* a, const float* b, size_t n) {
 using namespace kata;
 
 KATA_API size_t kata_fwd_linear_decay_workspace_size(int T, int H, int d, int dv, int N) {
-  if (check_shape(T, H, d, dv, N, KATA_BF16) != KATA_OK || T == 0 || N == 0) return 0;
+  if (check_shape(T, H, d, dv, N, KATA_BF16, 1) != KATA_OK || T == 0 || N == 0) return 0;
   return decay_workspace_bytes(T, H, d, dv, N, 1);
 }
 
@@ -60,7 +66,7 @@ KATA_API kata_status_t kata_fwd_linear_decay(const void* q, const void* k, const
                                              const int* slots, int n_slots, const unsigned char* resume,
                                              int zero_outside, kata_dtype_t dtype, void* workspace,
                                              size_t workspace_bytes, void* stream) {
-  kata_status_t s = check_shape(T, H, d, dv, N, dtype);
+  kata_status_t s = check_shape(T, H, d, dv, N, dtype, 1);
   if (s != KATA_OK) return s;
   if (dtype != KATA_BF16) return KATA_ERR_UNSUPPORTED;
   if (!cu_seqlens && N != 1) return KATA_ERR_INVALID_ARG;
@@ -95,7 +101,7 @@ KATA_API kata_status_t kata_fwd_linear_decay(const void* q, const void* k, const
 }
 
 KATA_API size_t kata_bwd_linear_decay_workspace_size(int T, int H, int d, int dv, int N) {
-  if (check_shape(T, H, d, dv, N, KATA_BF16) != KATA_OK || T == 0 || N == 0) return 0;
+  if (check_shape(T, H, d, dv, N, KATA_BF16, 3) != KATA_OK || T == 0 || N == 0) return 0;
   return decay_workspace_bytes(T, H, d, dv, N, 3);
 }
 
@@ -105,7 +111,7 @@ KATA_API kata_status_t kata_bwd_linear_decay(const void* q, const void* k, const
                                              const float* log_decay, float scale, const int* cu_seqlens, int N,
                                              const float* S0, const float* dS_out, float* dS0, kata_dtype_t dtype,
                                              void* workspace, size_t workspace_bytes, void* stream) {
-  kata_status_t s = check_shape(T, H, d, dv_width, N, dtype);
+  kata_status_t s = check_shape(T, H, d, dv_width, N, dtype, 3);
   if (s != KATA_OK) return s;
   if (dtype != KATA_BF16) return KATA_ERR_UNSUPPORTED;
   if (!cu_seqlens && N != 1) return KATA_ERR_INVALID_ARG;
@@ -150,9 +156,10 @@ KATA_API kata_status_t kata_decode_step_linear_decay(const void* q, const void* 
                                                      long long k_stride, long long v_stride, long long o_stride,
                                                      const float* log_decay, float scale, const int* slots,
                                                      int n_slots, kata_dtype_t dtype, void* stream) {
-  kata_status_t s = check_shape(0, H, d, dv, n, dtype);
+  kata_status_t s = check_shape(0, H, d, dv, n, dtype, 0);
   if (s != KATA_OK) return s;
   if ((long long)n * H * (dv / 32) > 0x7fffffffll) return KATA_ERR_UNSUPPORTED;
+  if (slots && (long long)n * n * H * (dv / 32) > kMaxStepSearch) return KATA_ERR_UNSUPPORTED;
   if (n_slots < 0 || (!slots && n_slots < n)) return KATA_ERR_INVALID_ARG;
   if (n == 0) return KATA_OK;
   if (!q || !k || !v || !o || (!S && n_slots > 0) || !log_decay) return KATA_ERR_INVALID_ARG;

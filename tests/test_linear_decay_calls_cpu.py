@@ -36,3 +36,27 @@ def test_states_of_one_call_may_lie_next_to_each_other(L, rows):
     # two states away the third row is shared; and with slots any of the nine may be
     assert _fwd(L, S0=ctypes.c_void_p(BASE + 2 * state), S_out=fresh, n_slots=9) == INVALID
     assert _fwd(L, S0=S0, S_out=fresh, n_slots=9, slots=P) == INVALID
+
+
+def test_calls_whose_search_would_hold_the_gpu_are_refused(L):
+    """The time of a call grows with the square of its sequences or streams; a call of a million would take minutes."""
+    assert _fwd(L, N=1 << 15, H=16, ks=16 * 64 + 4) == MISALIGNED  # half of the bound
+    assert _fwd(L, N=1 << 16, H=16, ks=16 * 64 + 4) == UNSUPPORTED
+    assert _fwd(L, N=1 << 20, H=1, ks=68) == UNSUPPORTED
+
+    def bwd(N, H):
+        return L.kata_bwd_linear_decay(P, P, P, P, P, P, P, 100, H, 64, 64, H * 64, H * 64 + 4, H * 64, P, 1.0, P, N,
+                                       None, None, None, 1, None, 0, None)
+
+    assert bwd(1 << 14, 16) == MISALIGNED and bwd(1 << 15, 16) == UNSUPPORTED
+
+    def step(n, H, dv, slots):
+        return L.kata_decode_step_linear_decay(P, P, P, P, P, n, H, 64, dv, H * 64, H * 64 + 2, H * dv, H * dv, P, 1.0,
+                                               slots, n, 1, None)
+
+    assert step(1 << 16, 16, 128, P) == MISALIGNED and step(1 << 20, 16, 128, P) == UNSUPPORTED
+    assert step(1 << 20, 16, 128, None) == MISALIGNED
+    assert step(1 << 20, 1, 64, P) == MISALIGNED
+    # what is refused needs no workspace, and a long call of one sequence is not refused
+    assert L.kata_fwd_linear_decay_workspace_size(1 << 22, 16, 64, 64, 1 << 16) == 0
+    assert L.kata_fwd_linear_decay_workspace_size(1 << 22, 16, 64, 64, 1) > 0
