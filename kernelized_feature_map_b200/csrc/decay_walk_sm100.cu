@@ -153,7 +153,7 @@ struct Shared {
   uint64_t sum_free[2];         // and read (128)
   uint64_t mma_done;            // every MMA issued has completed
   float keep[2];                // a^128, its rounded value and what that leaves out
-  float keep_segment;           // a^L
+  float keep_segment[2];        // a^L likewise
   uint32_t tmem;
   int abort;
 };
@@ -369,6 +369,15 @@ __device__ __forceinline__ int last_walked(const WalkParams& w, const Found& f) 
 // not, what rest would add to it is below 2^-21 of it, and hi and lo do.
 __device__ __forceinline__ bool remembered(float g, int tokens) { return g * (float)tokens >= -2.7725887f; }
 
+// a^tokens as a rounded value and what that leaves out: a state is multiplied by it
+// once a chunk or segment, for as long as it remembers, and rounding it every time
+// by 2^-25 the same way would add up (147 segments: 2e-6 of the state).
+__device__ __forceinline__ void power_of(float g, int tokens, float& hi, float& lo) {
+  const double x = exp((double)g * tokens);
+  hi = (float)x;
+  lo = (float)(x - (double)hi);
+}
+
 // y of the first weight
 __device__ __forceinline__ int first_weight(bool reverse) { return reverse ? -32 : -128; }
 
@@ -457,11 +466,12 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       for (int s = 0; s < before; ++s) {
         const int seg = rev ? f.n_seg - 1 - s : s;
         const int tokens = min(p.L, f.s1 - f.s0 - seg * p.L);
-        const float keep = tokens == p.L ? sh.keep_segment : expf(g * (float)tokens);
+        const float keep = tokens == p.L ? sh.keep_segment[0] : expf(g * (float)tokens);
+        const float more = tokens == p.L ? sh.keep_segment[1] : 0.f;
         float x[kCols];
         row_of(w.rec + ((long long)(f.rec + seg) * p.H + h) * size, x);
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) r[e] = fmaf(keep, r[e], x[e]);
+        for (int e = 0; e < kCols; ++e) r[e] = fmaf(keep, r[e], fmaf(more, r[e], x[e]));
       }
     }
     const uint32_t to = tmem + ((uint32_t)(warp % 4 * 32) << 16) + C::colS + at;
@@ -1038,11 +1048,8 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
       prefetch_tmap(&w.b);
       prefetch_tmap(&w.c);
       prefetch_tmap(&w.o);
-      // in double: the state is multiplied by it once a chunk, for as long as it remembers
-      const double keep = exp((double)g * kChunk);
-      sh.keep[0] = (float)keep;
-      sh.keep[1] = (float)(keep - (double)sh.keep[0]);
-      sh.keep_segment = (float)exp((double)g * p.L);
+      power_of(g, kChunk, sh.keep[0], sh.keep[1]);
+      power_of(g, p.L, sh.keep_segment[0], sh.keep_segment[1]);
     }
   } else if constexpr (!kSum) {
     for (int x = threadIdx.x - 128; x < 2 * kWeights; x += kThreads - 128) {
@@ -1136,12 +1143,8 @@ __global__ void __launch_bounds__(kScanThreads) decay_scan_kernel(const __grid_c
     const int seg = rev ? f.n_seg - 1 - s : s;
     return reinterpret_cast<float4*>(w.rec) + ((long long)(f.rec + seg) * p.H + h) * size4 + x;
   };
-  const float full = (float)exp((double)g * p.L);
-  auto factor = [&](int s) {
-    const int seg = rev ? f.n_seg - 1 - s : s;
-    const int tokens = min(p.L, f.s1 - f.s0 - seg * p.L);
-    return tokens == p.L ? full : expf(g * (float)tokens);
-  };
+  float full, rest;
+  power_of(g, p.L, full, rest);
   for (int s0 = 0; s0 < f.n_seg; s0 += kAhead) {
     float4 sum[kAhead];
 #pragma unroll
@@ -1152,9 +1155,10 @@ __global__ void __launch_bounds__(kScanThreads) decay_scan_kernel(const __grid_c
       if (s0 + u >= f.n_seg) break;
       *at(s0 + u) = e;
       if (s0 + u < f.n_seg - 1) {
-        const float k = factor(s0 + u);
-        e = make_float4(fmaf(k, e.x, sum[u].x), fmaf(k, e.y, sum[u].y), fmaf(k, e.z, sum[u].z),
-                        fmaf(k, e.w, sum[u].w));
+        const int seg = rev ? f.n_seg - 1 - s0 - u : s0 + u, tokens = min(p.L, f.s1 - f.s0 - seg * p.L);
+        const float k = tokens == p.L ? full : expf(g * (float)tokens), r = tokens == p.L ? rest : 0.f;
+        e = make_float4(fmaf(k, e.x, fmaf(r, e.x, sum[u].x)), fmaf(k, e.y, fmaf(r, e.y, sum[u].y)),
+                        fmaf(k, e.z, fmaf(r, e.z, sum[u].z)), fmaf(k, e.w, fmaf(r, e.w, sum[u].w)));
       }
     }
   }

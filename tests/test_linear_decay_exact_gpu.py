@@ -1,0 +1,142 @@
+"""How exact the states of linear attention with a per-head decay are, against
+64 bits.
+
+A state of tokens of like magnitude agrees with fp32 arithmetic.  In the 2-norm,
+relative to the state:
+* keys times their decay as three bf16 values lose 2^-24; those of chunks that
+  are less than a 16th of what leaves are two values, off by up to 2^-16, in the
+  mean square 2^-16 / sqrt(3) of less than 1/16: 5.5e-7;
+* the tensor cores truncate a chunk's sum 8 times (16 tokens a product) by up to
+  one step of 2^-23 of what it has come to, half a step in the mean, sqrt(i / 8)
+  of the chunk after i products: 8 * 0.71 * 2^-24 = 3.4e-7;
+* the decays' powers, the additions of the chunks and the factors between chunks
+  and between segments are off by a few 2^-25 each, and the factors not by more
+  for longer walks, being held as two fp32 values.
+Independent of one another: 6.6e-7, below 1e-6.  Keys of two bf16 values alone
+come to 3e-6 to 4.5e-6, and factors of one fp32 value to up to 2^-25 for every
+chunk or segment walked.
+"""
+import numpy as np
+import pytest
+import torch
+
+import kernelized_feature_map_b200 as K
+from kernelized_feature_map_b200 import _abi
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    from kernelized_feature_map_b200 import build
+    build.build()
+    torch.cuda.synchronize()
+    K.kata_get_status()
+    yield
+    torch.cuda.synchronize()
+    assert K.kata_get_status() == _abi.KATA_OK
+
+
+def gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def bf(g, *shape):
+    return torch.randn(shape, device="cuda", generator=g).to(torch.bfloat16)
+
+
+def edges(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def worst_rounded(near, tokens):
+    """A decay's logarithm near `near` whose power over `tokens` tokens fp32 rounds by almost half a step."""
+    g = (near * (1 + np.arange(4096) / 8192)).astype(np.float32)
+    x = np.exp(g.astype(np.float64) * tokens)
+    return float(g[np.argmax(np.abs(x.astype(np.float32) - x) / x)])
+
+
+def state(k, v, g, S0, reverse=False):
+    """The state that leaves one sequence, in 64 bits: [x, H, d], [x, H, dv], S0 [H, d, dv]; reversed it is the
+    gradient of the state that entered, of queries k and upstream gradients v."""
+    x, out = k.shape[0], []
+    t = torch.arange(x, device="cuda", dtype=torch.float64)
+    for h in range(k.shape[1]):
+        w = torch.exp(g[h].double() * (t + 1 if reverse else x - 1 - t))
+        out.append(torch.exp(g[h].double() * x) * S0[h].double() + (k[:, h].double() * w[:, None]).T @ v[:, h].double())
+    return torch.stack(out)
+
+
+def error(got, want):
+    """Largest relative error in the 2-norm over the heads."""
+    n = lambda x: torch.linalg.vector_norm(x.double(), dim=(-2, -1))  # noqa: E731
+    return float((n(got.double() - want) / n(want)).max())
+
+
+def parts(T, H, N, walks):
+    """T over the plan's length of segments, from the records it asks for (0: one segment)."""
+    f = K.kata_fwd_linear_decay_workspace_size if walks == 1 else K.kata_bwd_linear_decay_workspace_size
+    records = f(T, H, 64, 64, N) // (H * 64 * 64 * 4 * walks)
+    return records // 2 if records <= 2 * N else records - N
+
+
+RETENTION = [float(np.log1p(-2.0 ** -5)), float(np.log1p(-2.0 ** -12)), 0.0, -0.5, -0.1]
+# (heads, d, dv, lengths, decays: RETENTION or one near this whose powers over a chunk or segment round worst)
+CASES = {
+    "short": (5, 128, 128, [16, 100, 128, 300], None),
+    "uncut": (5, 64, 128, [1000] * 32, None),
+    "uncut slow": (16, 64, 64, [16384] * 10, -2.0 ** -17),
+    "folded": (16, 128, 64, [5000, 90, 1], None),
+    "folded slow": (16, 64, 64, [32768], -2.0 ** -17),
+    "scanned": (5, 128, 128, [5000, 90, 1], None),
+    "scanned slow": (1, 64, 64, [131072], -2.0 ** -18),
+}
+
+
+def decays(case, walks):
+    H, _, _, lens, slow = CASES[case]
+    T, N = sum(lens), len(lens)
+    if slow is None:
+        return torch.tensor([RETENTION[h % 5] for h in range(H)], dtype=torch.float32, device="cuda")
+    over = 128  # tokens whose power the state is multiplied by again and again
+    if not case.startswith("uncut"):  # a segment's, a multiple of 128
+        n = parts(T, H, N, walks)
+        over = T // n // 128 * 128
+        assert n > 1 and over > T / (n + 1)
+    return torch.full((H,), worst_rounded(slow, over), device="cuda")
+
+
+@pytest.mark.parametrize("case", list(CASES))
+def test_states_agree_with_fp32_arithmetic(case):
+    H, d, dv, lens, _ = CASES[case]
+    N, T, r, g = len(lens), sum(lens), gen(len(case)), decays(case, 1)
+    n = parts(T, H, N, 1)  # segments have at least T / (n + 1) tokens
+    if case.startswith("scanned"):
+        assert n >= 16
+    elif case.startswith("folded"):
+        assert 1 < n < 16
+    else:
+        assert n == 0 or max(lens) <= T / (n + 1)
+    k, v = bf(r, T, H, d), bf(r, T, H, dv)
+    S0 = torch.randn(N, H, d, dv, device="cuda", generator=r) * 4
+    S = K.kata_fwd_linear_decay(torch.zeros_like(k), k, v, g, edges(lens), 1.0, S0=S0, return_state=True)[1]
+    a = 0
+    for n, x in enumerate(lens):
+        e = error(S[n], state(k[a:a + x], v[a:a + x], g, S0[n]))
+        assert e <= 1e-6, (n, x, e)
+        a += x
+
+
+@pytest.mark.parametrize("case", [c for c in CASES if c != "uncut slow"])
+def test_gradients_of_entering_states_agree_with_fp32_arithmetic(case):
+    H, d, dv, lens, _ = CASES[case]
+    N, T, r, g = len(lens), sum(lens), gen(len(case)), decays(case, 3)
+    q, dO = bf(r, T, H, d), bf(r, T, H, dv)
+    dS = torch.randn(N, H, d, dv, device="cuda", generator=r) * 4
+    dS0 = K.kata_bwd_linear_decay(q, torch.zeros_like(q), torch.zeros_like(dO), dO, g, edges(lens), 1.0, dS_out=dS,
+                                  return_dS0=True)[3]
+    a = 0
+    for n, x in enumerate(lens):
+        e = error(dS0[n], state(q[a:a + x], dO[a:a + x], g, dS[n], reverse=True))
+        assert e <= 1e-6, (n, x, e)
+        a += x
