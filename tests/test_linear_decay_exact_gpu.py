@@ -1,5 +1,5 @@
-"""How exact the states of linear attention with a per-head decay are, against
-64 bits.
+"""How exact the states of linear attention with a per-head decay are, and its
+gradients at strong decays where sequences are cut, against 64 bits.
 
 A state of tokens of like magnitude agrees with fp32 arithmetic.  In the 2-norm,
 relative to the state:
@@ -140,3 +140,66 @@ def test_gradients_of_entering_states_agree_with_fp32_arithmetic(case):
         e = error(dS0[n], state(q[a:a + x], dO[a:a + x], g, dS[n], reverse=True))
         assert e <= 1e-6, (n, x, e)
         a += x
+
+
+@pytest.mark.parametrize("lens", [[400], [9000]])
+def test_a_state_whose_last_keys_are_zero(lens):
+    """Which keys are held as three values goes by the decay alone.  Where the last tokens add nothing, the state
+    that leaves is made of keys of two, off by up to 2^-16 each, 2^-16 / sqrt(3) = 8.8e-6 in the mean square."""
+    r, T, H, d = gen(5), sum(lens), 2, 64
+    g = torch.tensor([-0.1, -0.03], device="cuda")
+    k, v = bf(r, T, H, d), bf(r, T, H, d)
+    k[T - 200:] = 0
+    S = K.kata_fwd_linear_decay(k, k, v, g, edges(lens), 1.0, return_state=True)[1][0]
+    want = state(k, v, g, torch.zeros_like(S))
+    assert error(S, want) <= 9e-6
+    mag = state(k.abs(), v.abs(), g, torch.zeros_like(S))
+    assert ((S.double() - want).abs() <= 2.0 ** -15 * mag).all()
+
+
+# --------------------------------------------------------------------------
+# gradients at strong decays, cut
+# --------------------------------------------------------------------------
+U = 2.0 ** -8
+
+
+def pairs(q, k, v, dO, g, scale, S0, dS):
+    """dq, dk, dv and dS0 of one sequence from the sums over pairs, nothing divided by the decay; [x, H, *] in."""
+    x, out = q.shape[0], []
+    t = torch.arange(x, device="cuda", dtype=torch.float64)
+    away = t[:, None] - t[None, :]
+    for h in range(q.shape[1]):
+        a, b, c, d = (y[:, h].double() for y in (q, k, v, dO))
+        d = scale * d
+        gh = g[h].double()
+        w = torch.where(away > 0, torch.exp(gh * away.clamp(min=1)), (away == 0).double())
+        reach = torch.exp(gh * (t + 1))[:, None]
+        share = torch.where(t == x - 1, 1.0, torch.exp(gh * (x - 1 - t).clamp(min=1)))[:, None]
+        P = (d @ c.T) * w
+        out.append((P @ b + reach * (d @ S0[h].double().T), P.T @ a + share * (c @ dS[h].double().T),
+                    ((a @ b.T) * w).T @ d + share * (b @ dS[h].double()),
+                    torch.exp(gh * x) * dS[h].double() + (reach * a).T @ d))
+    return [torch.stack(y, 1) for y in list(zip(*out))[:3]] + [torch.stack([y[3] for y in out])]
+
+
+@pytest.mark.parametrize("H,d,dv,lens", [(6, 64, 64, [1500, 900, 3]), (5, 128, 64, [2000, 1, 129]), (12, 64, 128, [1700])])
+def test_gradients_cut_at_strong_decays(H, d, dv, lens):
+    """Decays from none to one that keeps only the current token, in one call whose sequences are cut.  Tolerances: u
+    = 2^-8 of the value and 1.02 u of the terms' magnitudes, for a state 2^-15 of these."""
+    r, N, T = gen(H + d), len(lens), sum(lens)
+    assert parts(T, H, N, 3) > 1
+    kinds = [-30.0, -float("inf"), -1.0, float(np.log1p(-2.0 ** -12)), 0.0, -3.0]
+    g = torch.tensor([kinds[h % 6] for h in range(H)], device="cuda")
+    q, k, v, dO = bf(r, T, H, d), bf(r, T, H, d), bf(r, T, H, dv), bf(r, T, H, dv)
+    S0, dS = (torch.randn(N, H, d, dv, device="cuda", generator=r) for _ in range(2))
+    got = K.kata_bwd_linear_decay(q, k, v, dO, g, edges(lens), 0.3, S0=S0, dS_out=dS, return_dS0=True)
+    a = 0
+    for n, x in enumerate(lens):
+        part = slice(a, a + x)
+        a += x
+        args = [y[part] for y in (q, k, v, dO)]
+        want = pairs(*args, g, 0.3, S0[n], dS[n])
+        mag = pairs(*[y.abs() for y in args], g, 0.3, S0[n].abs(), dS[n].abs())
+        for y, w, m in zip(got[:3], want, mag):
+            assert ((y[part].double() - w).abs() <= U * w.abs() + 1.02 * U * m + 1e-30).all()
+        assert ((got[3][n].double() - want[3]).abs() <= 2.0 ** -15 * mag[3] + 1e-30).all()
