@@ -880,6 +880,7 @@ def main():
     ap.add_argument("--long", type=int, default=1, help="also time the T=131072 workload (1 GPU)")
     ap.add_argument("--long-steps", type=int, default=8)
     ap.add_argument("--sweep", type=int, default=1, help="also time the B x T grid and the p=32 recall workload")
+    ap.add_argument("--detail", type=int, default=0, help="everything in the JSON line (default: on stderr)")
     ap.add_argument("--cpu-baseline", type=int, default=1)
     ap.add_argument("--graph", type=int, default=1, help="time the step as a CUDA graph replay (per-path times stay eager)")
     ap.add_argument("--ref-budget", type=float, default=15.0, help="seconds of oracle work per reference step")
@@ -926,7 +927,7 @@ def main():
         step_ms, e2e_ms = reduce_max([step_ms, e2e_ms], world, device="cuda")
         if rank != 0:
             return
-        report(args, res, step_ms, e2e_ms, world)
+        report(args, res, step_ms, e2e_ms, world, brief=not args.detail)
     finally:
         if world > 1:
             import torch.distributed as dist
@@ -1020,7 +1021,15 @@ def roofline_points(res, peaks, cfg):
     return pts
 
 
-def report(args, res, step_ms, e2e_ms, world):
+# What a reader of the benchmark's one line needs; the rest (other workloads, points for every path) made it longer
+# than the 3000 characters that are kept of a run's output.
+BRIEF_KEYS = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling",
+              "vs_baseline", "dtype", "data", "config", "roofline", "e2e", "gpu_launches", "clocks", "paths",
+              "timed_region_s", "kernel_status", "cpu_baseline")
+
+
+def report(args, res, step_ms, e2e_ms, world, brief=False):
+    """Print the JSON line; brief: the keys of BRIEF_KEYS on stdout, and everything on stderr behind "detail: "."""
     peaks, peak_src = load_peaks()
     cfg = workloads.CONFIGS[args.workload]
     BH, T, p, dv = res["BH"], res["T"], res["p"], res["dv"]
@@ -1169,6 +1178,10 @@ def report(args, res, step_ms, e2e_ms, world):
         cb = time_oracle(cfg)
         line["cpu_baseline"] = {"value": cb["value"], "unit": UNIT, "cores": cb["cores"], "kind": "oracle",
                                 "sample": cb["sample"]}
+    if brief:
+        print("detail: " + json.dumps(line), file=sys.stderr, flush=True)
+        line = {k: line[k] for k in BRIEF_KEYS if k in line}
+        line["roofline"] = {k: v for k, v in line["roofline"].items() if k != "points"}
     print(json.dumps(line), flush=True)
 
 

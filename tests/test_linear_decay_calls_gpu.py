@@ -97,7 +97,7 @@ def test_what_a_call_writes_is_known_to_autograd():
     r, H, d = gen(2), 2, 64
     x, g = bf(r, 5, H, d), torch.full((H,), -0.1, device="cuda")
     S = torch.randn(3, H, d, d, device="cuda", generator=r)
-    z, zc, sc = torch.zeros(3, H, d, device="cuda"), torch.zeros(3, H, d, device="cuda"), torch.zeros(3, H, d, device="cuda")
+    z, zc, sc = (torch.zeros(3, H, d, device="cuda") for _ in range(3))
     cache, o = torch.zeros(3, H, d, d, dtype=torch.int8, device="cuda"), torch.zeros_like(x)
     calls = [
         (lambda: K.kata_fwd_linear_decay(x, x, x, g, S0=S, return_state=True), []),

@@ -182,7 +182,8 @@ def pairs(q, k, v, dO, g, scale, S0, dS):
     return [torch.stack(y, 1) for y in list(zip(*out))[:3]] + [torch.stack([y[3] for y in out])]
 
 
-@pytest.mark.parametrize("H,d,dv,lens", [(6, 64, 64, [1500, 900, 3]), (5, 128, 64, [2000, 1, 129]), (12, 64, 128, [1700])])
+@pytest.mark.parametrize("H,d,dv,lens", [(6, 64, 64, [1500, 900, 3]), (5, 128, 64, [2000, 1, 129]),
+                                         (12, 64, 128, [1700])])
 def test_gradients_cut_at_strong_decays(H, d, dv, lens):
     """Decays from none to one that keeps only the current token, in one call whose sequences are cut.  Tolerances: u
     = 2^-8 of the value and 1.02 u of the terms' magnitudes, for a state 2^-15 of these."""
