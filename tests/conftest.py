@@ -24,3 +24,15 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+# MEASURED_PEAKS.json holds what a copy and a matrix product reached on the machine at hand, and changes with every
+# measurement; the report's expected fractions are those of this one.
+REPORT_PEAKS = {"hbm_gbs": 6551.0, "bf16_tflops": 1617.3, "bf16_tflops_sustained": 1379.0}
+
+
+@pytest.fixture(autouse=True)
+def report_peaks(request, monkeypatch):
+    if request.module.__name__ == "test_bench_cpu":
+        import bench
+        monkeypatch.setattr(bench, "load_peaks", lambda: (dict(REPORT_PEAKS), "measured"))
