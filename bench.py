@@ -52,10 +52,10 @@ UNIT = "tokens/s"
 # from the ncu capture summarised in profiles/flash_fwd_kernel_ctx2k.md (the
 # traffic recapture).  It is reported only while the kernel's sources are the
 # ones that capture ran.
-FLASH_TRAFFIC_BYTES = 50576640 + 6089984
+FLASH_TRAFFIC_BYTES = 50500608 + 5885440
 FLASH_TRAFFIC_SOURCES = ("kernelized_feature_map_b200/csrc/flash_sm100.cu", "kernelized_feature_map_b200/csrc/sm100.cuh",
                          "kernelized_feature_map_b200/csrc/kata_trace.cuh", "kernelized_feature_map_b200/csrc/kata_common.cuh")
-FLASH_TRAFFIC_SHA256 = "7f2726d66afacd6130957ecff278be8d9136251b02fe3e367a30c61ce87e8e25"
+FLASH_TRAFFIC_SHA256 = "409f903759864aafb77dd36b1a8aa5f9ef42088b4535b983b7fa273cceb35544"
 
 
 def flash_traffic(workload):

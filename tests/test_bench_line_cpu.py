@@ -26,3 +26,9 @@ def test_the_printed_line_is_short_and_the_details_are_on_stderr(capsys, monkeyp
     detail = json.loads(err.split("detail: ", 1)[1])
     assert {"mg", "train", "long_ctx"} <= set(detail) and detail["roofline"]["points"]
     assert all(detail[k] == line[k] for k in line if k != "roofline")
+
+
+def test_the_traffic_reported_is_that_of_the_present_sources():
+    """None once a source of the flash kernel has changed: the capture is then to be taken again."""
+    assert bench.flash_traffic("layer340m_ctx2k") == bench.FLASH_TRAFFIC_BYTES
+    assert bench.flash_traffic("another") is None
