@@ -153,7 +153,7 @@ struct Shared {
   uint64_t sum_free[2];         // and read (128)
   uint64_t mma_done;            // every MMA issued has completed
   float keep[2];                // a^128, its rounded value and what that leaves out
-  float keep_segment[2];        // a^L likewise
+  float keep_segment;           // a^L
   uint32_t tmem;
   int abort;
 };
@@ -370,8 +370,9 @@ __device__ __forceinline__ int last_walked(const WalkParams& w, const Found& f) 
 __device__ __forceinline__ bool remembered(float g, int tokens) { return g * (float)tokens >= -2.7725887f; }
 
 // a^tokens as a rounded value and what that leaves out: a state is multiplied by it
-// once a chunk or segment, for as long as it remembers, and rounding it every time
-// by 2^-25 the same way would add up (147 segments: 2e-6 of the state).
+// once a chunk (a scanned one: once a segment), for as long as it remembers, and
+// what rounding leaves out, up to 2^-25, would add up, the same every time (147
+// segments: 2e-6 of the state).
 __device__ __forceinline__ void power_of(float g, int tokens, float& hi, float& lo) {
   const double x = exp((double)g * tokens);
   hi = (float)x;
@@ -466,12 +467,11 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
       for (int s = 0; s < before; ++s) {
         const int seg = rev ? f.n_seg - 1 - s : s;
         const int tokens = min(p.L, f.s1 - f.s0 - seg * p.L);
-        const float keep = tokens == p.L ? sh.keep_segment[0] : expf(g * (float)tokens);
-        const float more = tokens == p.L ? sh.keep_segment[1] : 0.f;
+        const float keep = tokens == p.L ? sh.keep_segment : expf(g * (float)tokens);
         float x[kCols];
         row_of(w.rec + ((long long)(f.rec + seg) * p.H + h) * size, x);
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) r[e] = fmaf(keep, r[e], fmaf(more, r[e], x[e]));
+        for (int e = 0; e < kCols; ++e) r[e] = fmaf(keep, r[e], x[e]);
       }
     }
     const uint32_t to = tmem + ((uint32_t)(warp % 4 * 32) << 16) + C::colS + at;
@@ -1049,7 +1049,9 @@ __global__ void __launch_bounds__(kSum ? kSumThreads : kThreads, 1) decay_walk_k
       prefetch_tmap(&w.c);
       prefetch_tmap(&w.o);
       power_of(g, kChunk, sh.keep[0], sh.keep[1]);
-      power_of(g, p.L, sh.keep_segment[0], sh.keep_segment[1]);
+      // rounded: up to 15 segments come to 3e-7 of the state in the mean square (what it leaves out, added here too,
+      // takes 1% of a packed batch's time)
+      sh.keep_segment = (float)exp((double)g * p.L);
     }
   } else if constexpr (!kSum) {
     for (int x = threadIdx.x - 128; x < 2 * kWeights; x += kThreads - 128) {

@@ -9,10 +9,11 @@ relative to the state:
 * the tensor cores truncate a chunk's sum 8 times (16 tokens a product) by up to
   one step of 2^-23 of what it has come to, half a step in the mean, sqrt(i / 8)
   of the chunk after i products: 8 * 0.71 * 2^-24 = 3.4e-7;
-* the decays' powers, the additions of the chunks and the factors between chunks
-  and between segments are off by a few 2^-25 each, and the factors not by more
-  for longer walks, being held as two fp32 values.
-Independent of one another: 6.6e-7, below 1e-6.  Keys of two bf16 values alone
+* the factors between chunks, and between 16 segments or more, are held as two
+  fp32 values; that between fewer segments is off by up to 2^-25 the same way
+  for each of up to 15, 9 in the mean square: 2.7e-7;
+* the decays' powers and the additions of the chunks are off by a few 2^-25.
+Independent of one another: 7.0e-7, below 1e-6.  Keys of two bf16 values alone
 come to 3e-6 to 4.5e-6, and factors of one fp32 value to up to 2^-25 for every
 chunk or segment walked.
 """
