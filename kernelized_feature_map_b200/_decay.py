@@ -51,7 +51,9 @@ def kata_fwd_linear_decay(q, k, v, log_decay, cu_seqlens=None, scale=1.0, S0=Non
     multiple of 16 bytes), so the parts of a fused projection go in as they
     are.  All tensors are on one device, which need not be the current one.
     With stream (a torch.cuda.Stream) the call runs there instead of on the
-    current stream, and what it allocates belongs to that stream.
+    current stream, and what it allocates belongs to that stream; the caller
+    keeps its own tensors until the call has run there (record_stream).
+    S_out and o, where given, are written in place, which autograd learns.
     """
     return (_native or _load()).fwd(q, k, v, log_decay, cu_seqlens, scale, S0, S_out, slots, resume, return_state,
                                     zero_outside, o, workspace, stream)

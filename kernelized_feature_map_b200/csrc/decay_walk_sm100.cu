@@ -17,11 +17,17 @@
 // Roundings.  S is fp32, in TMEM for the whole walk.  The tensor cores truncate
 // as they accumulate, so U is summed for itself, smallest part first, and added
 // to S by the CUDA cores; a^128 is held as the sum of two fp32 values.  A scaled
-// key enters U as two bf16 values (it loses 2^-17), as three (2^-25) where the
-// chunk is still an 1/16 or more of the state that leaves: that state then
-// agrees with fp32 arithmetic (1e-7 to 3e-7 of it in the mean square).  W and
-// the copy of S that A is multiplied with are rounded to bf16 once: they reach
-// only out, which is rounded as far itself.
+// key enters U as two bf16 values (it loses up to 2^-16), as three (2^-24) where
+// the chunk is still an 1/16 or more of the state that leaves.  Of tokens of like
+// magnitude that state then agrees with fp32 arithmetic (1e-7 to 3e-7 of it in the
+// mean square, at any length).  Which it is goes by the decay alone: where the last
+// tokens' keys are zero or small, the state is made of keys of two values, and off
+// by up to 9e-6 (4.8e-6 measured; with three everywhere 131072 tokens take 935 us
+// instead of 760, 8192 in 13 sequences 89 instead of 82).  W and the copy of S that A is multiplied with are rounded to
+// bf16 once, as operands of the tensor cores: they reach only out, which is rounded
+// as far itself.  Out's error is 0.0024 in the mean square, of which its own
+// rounding is 0.0017; a second value of each would be eight products more, and a
+// second copy of S has no room beside two stages at d = dv = 128.
 //
 // One CTA per segment of a sequence, head and walk (1 CTA per SM: 512 TMEM
 // columns, 26 warps of 72 registers):
@@ -55,11 +61,10 @@
 // works 38%; its tiles cross shared memory in 4700 cycles, and at 148 SMs its
 // bytes HBM in 5500.  The sums, of which no chunk waits for another, are bound by
 // the loads in flight (three stages 4.6 TB/s, two 3.7).  Measured: 131072 tokens,
-// 16 heads, d = dv = 128 650 to 710 us, 3.2 TB/s of q, k, v and o (780 us among
-// other work, under the power cap); a quarter of it are the segments' sums, which
-// read k and v once more.  8192 tokens in 13
-// sequences: 81 us.  75 tokens, d = dv = 64: 8.3 us, a launch and one chunk's path.
-// Gradients, 8 x 2048 tokens, 16 heads, d = dv = 128: 190 to 220 us.  Tried and not
+// 16 heads, d = dv = 128 730 us, 2.9 TB/s of q, k, v and o (650 to 780 us by the
+// clocks that the power cap leaves); a quarter of it are the segments' sums, which
+// read k and v once more.  8192 tokens in 13 sequences: 83 us.  75 tokens, d = dv = 64: 8.3 us, a launch and one chunk's path.
+// Gradients, 8 x 2048 tokens, 16 heads, d = dv = 128: 195 us.  Tried and not
 // faster: fewer warps with more registers each, out by warps of its own, two
 // accumulators for out, A S ahead of P, W in blocks of 32 columns (spills), S with
 // its next columns on their way, a quarter of S by the warps of W.
@@ -282,8 +287,8 @@ __device__ __forceinline__ void scale_columns(uint32_t col, float factor) {
 // A key times its factor, f k, as the sum of three bf16 values: hi = f1 k with f1
 // the factor rounded, lo = (f1 k - hi) + f2 k with f2 what f1 leaves out (the
 // parenthesis is a bf16 value), and rest what these leave out, from the product
-// in fp32.  Up to 2^-25 of f k is lost, as in fp32 arithmetic; hi and lo alone
-// would lose 2^-17 (4e-6 of the state in the mean square).  Rows past the end
+// in fp32.  Up to 2^-24 of f k is lost, as in fp32 arithmetic; hi and lo alone
+// would lose 2^-16 (4e-6 of the state in the mean square).  Rows past the end
 // (another sequence's, or nothing) count as zeros, and are cleared in the tiles.
 struct KeyFactor {
   __nv_bfloat162 f1, f2;
@@ -366,7 +371,8 @@ __device__ __forceinline__ int last_walked(const WalkParams& w, const Found& f) 
 }
 
 // Whether a state still holds a 16th or more of what entered it `tokens` ago.  If
-// not, what rest would add to it is below 2^-21 of it, and hi and lo do.
+// not, what rest would add to it is below 2^-20 of the size it entered with, and hi
+// and lo do: 2^-20 of the state where later tokens are as large as earlier ones.
 __device__ __forceinline__ bool remembered(float g, int tokens) { return g * (float)tokens >= -2.7725887f; }
 
 // a^tokens as a rounded value and what that leaves out: a state is multiplied by it
@@ -809,7 +815,6 @@ __device__ void walk(const Params& p, const WalkParams& w, int h, float g, uint8
 #pragma unroll
         for (int e = 0; e < D1 / 4; ++e) {
           x[e] = kf.low(x[e]);
-          
         }
         if (!wait(a_done, c & 1)) break;
         write_half<D1>(tA, j, half, x, [](uint32_t k) { return k; });
@@ -1216,6 +1221,16 @@ bool make_tmap(CUtensorMap* map, const void* base, int width, int H, int T, long
 // would outlast the rest; and several short sequences (up to kUncut chunks
 // together) never, as even two more launches that find nothing to do cost
 // 6 us (a call of 1337 tokens in 5 sequences 37 us instead of 27).
+//
+// kUncut measured, cut against not, calls of 2, 5 and 12 sequences of very unequal
+// lengths, 2 to 24 heads, us: 10 chunks together 19.4 against 20.3 at best (2
+// sequences, 2 heads, d = dv = 64), everywhere else not cutting is faster, by 10 to
+// 70%.  12 chunks: two sequences 20.7 against 24.8 (d = dv = 64) and 34.8 against
+// 34.4 (128), five 19.9 against 15.9 and 28.7 against 22.0.  14 chunks: two 24.1
+// against 38.1 and 41.6 against 51.8, five 22.3 against 26.8 and 35.5 against 37.0,
+// twelve 18.8 against 15.8 and 30.5 against 21.7.  What decides is the longest
+// sequence (cutting pays from 8 chunks on at 64, from 9 at 128, if few heads leave
+// SMs free), which the plan does not know.
 struct Plan {
   int L;              // tokens per segment, a multiple of 128
   int max_segments;   // of all sequences together

@@ -205,3 +205,38 @@ def test_gradients_cut_at_strong_decays(H, d, dv, lens):
         for y, w, m in zip(got[:3], want, mag):
             assert ((y[part].double() - w).abs() <= U * w.abs() + 1.02 * U * m + 1e-30).all()
         assert ((got[3][n].double() - want[3]).abs() <= 2.0 ** -15 * mag[3] + 1e-30).all()
+
+
+@pytest.mark.parametrize("H,d,dv,lens", [(2, 64, 64, [90, 140]), (1, 128, 64, [2600])])
+def test_gradients_against_differences(H, d, dv, lens):
+    """(f(x + u) - f(x - u)) / 2 of f = sum(o dO) + sum(S dS), each input in turn, on small integers: x + u and x - u
+    are bf16 values, and f is linear in each input, so that only the roundings of o, S and the gradients are off: 3 u
+    of the terms' magnitudes each (2 u in o, both sides of the difference, and 2 u in the gradient), independent of
+    one another: their sum is off by the root of the sum of their squares."""
+    r, N, T = gen(d), len(lens), sum(lens)
+    whole = lambda n, *shape: torch.randint(-n, n + 1, shape, device="cuda", generator=r).float()  # noqa: E731
+    x = [whole(4, T, H, d), whole(4, T, H, d), whole(4, T, H, dv), whole(4, N, H, d, dv)]
+    dO, dS = whole(3, T, H, dv).to(torch.bfloat16), whole(3, N, H, d, dv)
+    g, cu, half = torch.tensor([-0.02, -0.3][:H], device="cuda"), edges(lens), torch.bfloat16
+
+    def forward(q, k, v, S0):
+        return K.kata_fwd_linear_decay(q.to(half), k.to(half), v.to(half), g, cu, 0.25, S0=S0, return_state=True)
+
+    def backward(q, k, v, S0, dO, dS):
+        return K.kata_bwd_linear_decay(q.to(half), k.to(half), v.to(half), dO, g, cu, 0.25, S0=S0, dS_out=dS,
+                                       return_dS0=True)
+
+    grads = backward(*x, dO, dS)
+    sizes = backward(*[t.abs() for t in x], dO.abs(), dS.abs())
+    mag_o, mag_S = forward(*[t.abs() + 2 for t in x])  # no smaller than those of x + u and x - u
+    for i in range(4):
+        u = whole(2, *x[i].shape)
+        up, down = list(x), list(x)
+        up[i], down[i] = x[i] + u, x[i] - u
+        (o1, S1), (o0, S0) = forward(*up), forward(*down)
+        dot = lambda a, b: (a.double() * b.double()).sum()  # noqa: E731
+        diff = (dot(o1, dO) - dot(o0, dO) + dot(S1, dS) - dot(S0, dS)) / 2
+        noise = torch.stack([dot(a * b, a * b) for a, b in ((3 * U * mag_o.double(), dO.double()),
+                                                            (2.0 ** -14 * mag_S.double(), dS.double()),
+                                                            (3 * U * sizes[i].double(), u.double()))]).sum().sqrt()
+        assert abs(diff - dot(grads[i], u)) <= noise, (i, float(diff), float(dot(grads[i], u)), float(noise))

@@ -10,7 +10,9 @@ Tolerances, u = 2^-8 being half a bf16 step relative to the value:
   2-norm the roundings are independent and at most u / sqrt(3) each: u.
 * an fp32 state: k times its decay is held as two bf16 values, off by at most
   u^2 = 2^-16 relative, 2^-16 / 3 in the mean square; with the fp32 sums
-  elementwise 2^-15 M and 1e-5 relative to the 2-norm.
+  elementwise 2^-15 M and 1e-5 relative to the 2-norm.  (Three values where the
+  state that leaves holds a 16th or more of them: test_linear_decay_exact_gpu.py
+  has the closer bound.)
 * one token in fp32: a few roundings of 2^-24; the sums over up to 128 terms
   (in the state, over the steps walked) 2^-24 each: 128 * 2^-24 M.
 """
