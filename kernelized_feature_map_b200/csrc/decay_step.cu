@@ -12,8 +12,8 @@
 // through shuffles and one shared-memory pass.
 //
 // Measured (other pools in between): 512 streams, 16 heads, d = dv = 128 1.07 GB in
-// 160 us, 6.7 TB/s (as a plain copy); 64 streams 22.6 us, 5.9 TB/s; 333 streams, 8
-// heads, d = 64, fp32 29 us, 6.0 TB/s; a single stream 2.7 us, a launch's latency
+// 160 us, 6.7 TB/s (as a plain copy); 64 streams 23.2 us, 5.8 TB/s; 333 streams, 8
+// heads, d = 64, fp32 29.1 us, 5.8 TB/s; a single stream 2.7 us, a launch's latency
 // (4.4 to 4.9 us a call, the host's part).
 #include "decay_common.cuh"
 #include "kata_internal.h"
