@@ -141,3 +141,51 @@ def test_gradients_that_start_anywhere_in_memory():
     up = [torch.cat([torch.zeros(3, dtype=t.dtype, device="cuda"), t.flatten()]) for t in (dO, dS)]
     got = torch.autograd.grad(flat, leaves, up)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_states_behind_two_to_the_31_elements():
+    """The last slots of a pool, and entries of a cache, of more elements than 32 bits count."""
+    n, H, d = 140000, 1, 128
+    r, last = gen(6), n - 1
+    pool = torch.empty(n, H, d, d, device="cuda")
+    cache, scale = torch.empty(n, H, d, d, dtype=torch.int8, device="cuda"), torch.empty(n, H, d, device="cuda")
+    z, zc = torch.empty(n, H, d, device="cuda"), torch.empty(n, H, d, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    first = torch.randn(1, H, d, d, device="cuda", generator=r)
+    pool[last - 1], z[last - 1] = first[0], first[0, :, :, 0]
+    K.kata_state_store_q8(pool, cache, scale, slots=i32(last - 1), entries=i32(last), z=z, z_cache=zc)
+    K.kata_state_load_q8(cache, scale, pool, entries=i32(last), slots=i32(last), z=z, z_cache=zc)
+    small = [torch.empty_like(t[:1]) for t in (cache, scale, pool)]
+    K.kata_state_store_q8(first, small[0], small[1])
+    K.kata_state_load_q8(small[0], small[1], small[2])
+    assert torch.equal(cache[last], small[0][0]) and torch.equal(pool[last], small[2][0])
+    assert torch.equal(z[last], first[0, :, :, 0])
+    g, S = torch.tensor([-0.1], device="cuda"), small[2].clone()
+    x = [bf(r, 1, H, d) for _ in range(3)]
+    o = K.kata_decode_step_linear_decay(*x, pool, g, slots=i32(last))
+    assert torch.equal(o, K.kata_decode_step_linear_decay(*x, S, g)) and torch.equal(pool[last], S[0])
+    for T in (50, 5000):  # whole, and cut
+        x = [bf(r, T, H, d) for _ in range(3)]
+        o = K.kata_fwd_linear_decay(*x, g, scale=0.1, S0=pool, S_out=pool, slots=i32(last))
+        want, S = K.kata_fwd_linear_decay(*x, g, scale=0.1, S0=S, return_state=True)
+        assert torch.equal(o, want) and torch.equal(pool[last], S[0])
+
+
+def test_tokens_behind_two_to_the_31_elements():
+    """Parts of a projection so wide that the last tokens lie behind 2^31 elements, and an output likewise."""
+    T, H, d, wide = 3001, 1, 64, 1 << 20
+    r, cu = gen(7), edges([2900, 1, 100])
+    rows = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")
+    parts = [rows[:, 64 * i:64 * i + 64].view(T, H, d) for i in (0, 1, 16000, 5)]
+    dense = [bf(r, T, H, d) for _ in range(3)]
+    for t, x in zip(parts, dense):
+        t.copy_(x)
+    g = torch.tensor([-0.01], device="cuda")
+    o = K.kata_fwd_linear_decay(*parts[:3], g, cu, 0.1, o=parts[3])
+    assert torch.equal(o, K.kata_fwd_linear_decay(*dense, g, cu, 0.1))
+    assert all(torch.equal(t, x) for t, x in zip(parts, dense))
+    dO = bf(r, T, H, d)
+    got = K.kata_bwd_linear_decay(*parts[:3], dO, g, cu, 0.1)
+    assert all(torch.equal(a, b) for a, b in zip(got, K.kata_bwd_linear_decay(*dense, dO, g, cu, 0.1)))
+    o1 = K.kata_decode_step_linear_decay(*parts[:3], torch.zeros(T, H, d, d, device="cuda"), g)
+    assert torch.equal(o1, K.kata_decode_step_linear_decay(*dense, torch.zeros(T, H, d, d, device="cuda"), g))
