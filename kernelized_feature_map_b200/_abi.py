@@ -138,6 +138,15 @@ def _written(*tensors):
     torch.autograd.graph.increment_version([t for t in tensors if t is not None])
 
 
+def _upstream(g):
+    """An upstream gradient as the kernels read it: dense, from 16 bytes on (what is cut from a larger gradient, as
+    behind a concatenation, may start anywhere)."""
+    if g is None:
+        return None
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 def kata_fwd_quadratic(q, k, v, o=None, stream=None):
     """Flash-style O(T^2) forward.  q,k [B,H,T,p], v [B,H,T,dv] -> o [B,H,T,dv]."""
     B, H, T, p = q.shape
@@ -355,7 +364,7 @@ class KataAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dO):
         q, k, v, o, D = ctx.saved_tensors
-        return kata_bwd_quadratic(q, k, v, o, D, dO.contiguous())
+        return kata_bwd_quadratic(q, k, v, o, D, _upstream(dO))
 
 
 def kata_attention(q, k, v):
@@ -435,7 +444,7 @@ class KataAttentionChunked(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dO):
         q, k, v, o, D = ctx.saved_tensors
-        return kata_bwd_chunked(q, k, v, o, D, dO.contiguous())
+        return kata_bwd_chunked(q, k, v, o, D, _upstream(dO))
 
 
 def kata_attention_chunked(q, k, v):
@@ -489,7 +498,7 @@ class KataAttentionMg(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dO):
         q, k, v, o, D = ctx.saved_tensors
-        dq, dk, dv = kata_bwd_mg_quadratic(q, k, v, o, D, dO.contiguous(), ctx.groups)
+        dq, dk, dv = kata_bwd_mg_quadratic(q, k, v, o, D, _upstream(dO), ctx.groups)
         return dq, dk, dv, None
 
 
@@ -544,7 +553,7 @@ class KataAttentionSg(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dO):
         q, k, v, o, D = ctx.saved_tensors
-        dq, dk, dv = kata_bwd_sg_quadratic(q, k, v, o, D, dO.contiguous(), ctx.groups)
+        dq, dk, dv = kata_bwd_sg_quadratic(q, k, v, o, D, _upstream(dO), ctx.groups)
         return dq, dk, dv, None
 
 

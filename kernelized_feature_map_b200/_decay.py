@@ -7,7 +7,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._abi import KataError, lib
+from ._abi import KataError, _upstream, lib
 
 _native = None
 
@@ -67,15 +67,6 @@ def kata_bwd_linear_decay(q, k, v, dO, log_decay, cu_seqlens=None, scale=1.0, S0
     get zeros; the decays get no gradient."""
     return (_native or _load()).bwd(q, k, v, dO, log_decay, cu_seqlens, scale, S0, dS_out, return_dS0, workspace,
                                     stream)
-
-
-def _upstream(g):
-    """An upstream gradient as the kernels read it: dense, from 16 bytes on (what is cut from a larger gradient, as
-    behind a concatenation, may start anywhere)."""
-    if g is None:
-        return None
-    g = g.contiguous()
-    return g if g.data_ptr() % 16 == 0 else g.clone()
 
 
 class KataAttentionLinearDecay(torch.autograd.Function):

@@ -1,5 +1,6 @@
 """What the calls on tensors write in place (states, outputs that are given) is
-known to autograd: torch's version counter of it rises, and of nothing else."""
+known to autograd: torch's version counter of it rises, and of nothing else.  And
+the differentiable functions take a gradient from anywhere in memory."""
 import pytest
 import torch
 
@@ -55,3 +56,17 @@ def test_inference_tensors_have_no_version():
         K.kata_decode_step(q, k, v, S, z)
     K.kata_decode_step(q, k, v, S, z)
     assert S.any()
+
+
+@pytest.mark.parametrize("path", ["flash", "chunked", "mg", "sg"])
+def test_gradients_that_start_anywhere_in_memory(path):
+    """The output behind a concatenation of flat tensors: its gradient is dense, but starts on 2 bytes."""
+    B, H, T, dv = 1, 2, 150, 64
+    d = 16 if path in ("flash", "chunked") else 32
+    q, k, v = _x(B, H, T, d).requires_grad_(), _x(B, H, T, d).requires_grad_(), _x(B, H, T, dv).requires_grad_()
+    o = {"flash": lambda: K.kata_attention(q, k, v), "chunked": lambda: K.kata_attention_chunked(q, k, v),
+         "mg": lambda: K.kata_attention_mg(q, k, v, 2), "sg": lambda: K.kata_attention_sg(q, k, v, 2)}[path]()
+    dO, pad = _x(B, H, T, dv), torch.zeros(3, dtype=torch.bfloat16, device="cuda")
+    want = torch.autograd.grad(o, (q, k, v), dO, retain_graph=True)
+    got = torch.autograd.grad(torch.cat([pad, o.flatten()]), (q, k, v), torch.cat([pad, dO.flatten()]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
