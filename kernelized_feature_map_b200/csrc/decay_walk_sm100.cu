@@ -23,11 +23,12 @@
 // mean square, at any length).  Which it is goes by the decay alone: where the last
 // tokens' keys are zero or small, the state is made of keys of two values, and off
 // by up to 9e-6 (4.8e-6 measured; with three everywhere 131072 tokens take 935 us
-// instead of 760, 8192 in 13 sequences 89 instead of 82).  W and the copy of S that A is multiplied with are rounded to
-// bf16 once, as operands of the tensor cores: they reach only out, which is rounded
-// as far itself.  Out's error is 0.0024 in the mean square, of which its own
-// rounding is 0.0017; a second value of each would be eight products more, and a
-// second copy of S has no room beside two stages at d = dv = 128.
+// instead of 760, 8192 in 13 sequences 89 instead of 82).  W and the copy of S that
+// A is multiplied with are rounded to bf16 once, as operands of the tensor cores:
+// they reach only out, which is rounded as far itself.  Out's error is 0.0024 in
+// the mean square, of which its own rounding is 0.0017; a second value of each
+// would be eight products more, and a second copy of S has no room beside two
+// stages at d = dv = 128.
 //
 // One CTA per segment of a sequence, head and walk (1 CTA per SM: 512 TMEM
 // columns, 26 warps of 72 registers):
@@ -63,11 +64,12 @@
 // the loads in flight (three stages 4.6 TB/s, two 3.7).  Measured: 131072 tokens,
 // 16 heads, d = dv = 128 730 us, 2.9 TB/s of q, k, v and o (650 to 780 us by the
 // clocks that the power cap leaves); a quarter of it are the segments' sums, which
-// read k and v once more.  8192 tokens in 13 sequences: 83 us.  75 tokens, d = dv = 64: 8.3 us, a launch and one chunk's path.
-// Gradients, 8 x 2048 tokens, 16 heads, d = dv = 128: 195 us.  Tried and not
-// faster: fewer warps with more registers each, out by warps of its own, two
-// accumulators for out, A S ahead of P, W in blocks of 32 columns (spills), S with
-// its next columns on their way, a quarter of S by the warps of W.
+// read k and v once more.  8192 tokens in 13 sequences: 83 us.  75 tokens, d = dv
+// = 64: 8.3 us, a launch and one chunk's path.  Gradients, 8 x 2048 tokens, 16
+// heads, d = dv = 128: 195 us.  Tried and not faster: fewer warps with more
+// registers each, out by warps of its own, two accumulators for out, A S ahead of
+// P, W in blocks of 32 columns (spills), S with its next columns on their way, a
+// quarter of S by the warps of W.
 #include <cuda.h>
 
 #include <algorithm>
@@ -1223,14 +1225,15 @@ bool make_tmap(CUtensorMap* map, const void* base, int width, int H, int T, long
 // 6 us (a call of 1337 tokens in 5 sequences 37 us instead of 27).
 //
 // kUncut measured, cut against not, calls of 2, 5 and 12 sequences of very unequal
-// lengths, 2 to 24 heads, us: 10 chunks together 19.4 against 20.3 at best (2
-// sequences, 2 heads, d = dv = 64), everywhere else not cutting is faster, by 10 to
-// 70%.  12 chunks: two sequences 20.7 against 24.8 (d = dv = 64) and 34.8 against
-// 34.4 (128), five 19.9 against 15.9 and 28.7 against 22.0.  14 chunks: two 24.1
-// against 38.1 and 41.6 against 51.8, five 22.3 against 26.8 and 35.5 against 37.0,
-// twelve 18.8 against 15.8 and 30.5 against 21.7.  What decides is the longest
-// sequence (cutting pays from 8 chunks on at 64, from 9 at 128, if few heads leave
-// SMs free), which the plan does not know.
+// lengths, 2 to 24 heads, us: 10 chunks together, two sequences of 2 heads at d =
+// dv = 64 19.4 against 20.3 (gradients 17.4, 18.8), all others lose by cutting, up
+// to 60% (128, 24 heads, gradients: 43.8, 27.2).  12 chunks: two sequences 20.7
+// against 24.8 (d = dv = 64) and 34.8 against 34.4 (128), five 19.9 against 15.9
+// and 28.7 against 22.0.  14 chunks: two 24.1 against 38.1 and 41.6 against 51.8,
+// five 22.3 against 26.8 and 35.5 against 37.0, twelve 18.8 against 15.8 and 30.5
+// against 21.7.  What decides is the longest sequence (cutting pays from 8 chunks
+// on at 64, from 9 at 128, if few heads leave SMs free), which the plan does not
+// know.
 struct Plan {
   int L;              // tokens per segment, a multiple of 128
   int max_segments;   // of all sequences together
@@ -1349,8 +1352,8 @@ cudaError_t launch_decay_empty(const DecayWalk& w, const DecayShape& sh, const W
   if (!w.fin) return cudaSuccess;
   const long long size4 = (long long)sh.H * w.d1 * w.d2 / 4;
   const long long tiles = std::min((size4 + kEmptyThreads - 1) / kEmptyThreads, (long long)kMaxGridRows);
-  decay_empty_kernel<<<dim3((unsigned)sh.N, (unsigned)tiles), kEmptyThreads, 0, st>>>(w.init, w.fin, sh.slots, sh.n_slots,
-                                                                                      sh.resume, size4, wc.status);
+  decay_empty_kernel<<<dim3((unsigned)sh.N, (unsigned)tiles), kEmptyThreads, 0, st>>>(
+      w.init, w.fin, sh.slots, sh.n_slots, sh.resume, size4, wc.status);
   return cudaGetLastError();
 }
 
