@@ -117,7 +117,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 def _stream_ptr(stream):
     s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _dev(t, name):
@@ -125,17 +125,20 @@ def _dev(t, name):
         raise TypeError("%s must be a CUDA tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _opt(t, name):
     return None if t is None else _dev(t, name)
 
 
+_increment_version = torch.autograd.graph.increment_version
+
+
 def _written(*tensors):
     """Tell autograd what a call has written: a backward pass whose saved
     tensors were written since is an error then, not a wrong gradient."""
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+    _increment_version([t for t in tensors if t is not None])
 
 
 def _upstream(g):

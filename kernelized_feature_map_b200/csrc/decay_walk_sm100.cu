@@ -1225,9 +1225,10 @@ bool make_tmap(CUtensorMap* map, const void* base, int width, int H, int T, long
 // 6 us (a call of 1337 tokens in 5 sequences 37 us instead of 27).
 //
 // kUncut measured, cut against not, calls of 2, 5 and 12 sequences of very unequal
-// lengths, 2 to 24 heads, us: 10 chunks together, two sequences of 2 heads at d =
-// dv = 64 19.4 against 20.3 (gradients 17.4, 18.8), all others lose by cutting, up
-// to 60% (128, 24 heads, gradients: 43.8, 27.2).  12 chunks: two sequences 20.7
+// lengths, 2 to 24 heads, us: 10 chunks together, two sequences of 2 and 8 heads at
+// d = dv = 64 19.4 and 19.8 against 20.3 and 20.6 (gradients of 2 heads 17.4, 18.8),
+// all others lose by cutting, up to 60% (128, 24 heads, gradients: 43.8, 27.2).
+// 12 chunks: two sequences 20.7
 // against 24.8 (d = dv = 64) and 34.8 against 34.4 (128), five 19.9 against 15.9
 // and 28.7 against 22.0.  14 chunks: two 24.1 against 38.1 and 41.6 against 51.8,
 // five 22.3 against 26.8 and 35.5 against 37.0, twelve 18.8 against 15.8 and 30.5
